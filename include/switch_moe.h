@@ -70,7 +70,10 @@ typedef enum {
  * its gate, and the result is rounded once. */
 typedef enum {
     SWITCH_F32 = 0,  /* IEEE binary32 */
-    SWITCH_BF16 = 1  /* bfloat16 */
+    SWITCH_BF16 = 1, /* bfloat16 */
+    SWITCH_E4M3 = 2  /* 8-bit float (4 exponent, 3 mantissa bits, no infinities, largest 448) with a
+                        float32 scale per row: the value is q * scale.  switch_layer_fwd_few's
+                        experts and x, switch_norm_fwd's and switch_quantize_rows' output only */
 } switch_dtype_t;
 
 /* Diagnostic switches for switch_dims_t.flags. */
@@ -313,6 +316,96 @@ switch_status_t switch_layer_bwd(const switch_dims_t *dims, const void *x, const
                                  const int32_t *counts, const float *dy, float g_aux, float *dx, float *dw_r,
                                  float *dbias, float *dw_in, float *dw_out, void *workspace, size_t workspace_bytes,
                                  switch_stream_t stream);
+
+/* ---- the layer for a few tokens -----------------------------------------
+ * The whole layer, top-1 or top-2, for the token group of a decoding step
+ * (T <= SWITCH_FEW_MAX_TOKENS): what switch_layer_fwd / switch_layer_fwd_top2
+ * compute, in two kernels bound by reading the weights of the experts that the
+ * tokens reach.  Outputs and readings (ties, capacity, the order of slots,
+ * aux) are those calls'; what differs:
+ *  - the hidden activations are not rounded to bfloat16: y carries float32
+ *    rounding only (about 1e-6 relative) beyond that of the given inputs;
+ *  - the experts may be SWITCH_E4M3 (dims.dtype), with a float32 scale per
+ *    output row (w_in_scale [N, F], w_out_scale [N, d]: W = q * scale); x is
+ *    then bfloat16, or SWITCH_E4M3 too, with a scale per token (x_scale [T]).
+ *    For other experts the three scale pointers must be NULL.
+ *  top_k     1 or 2 (N >= top_k); expert, gate and slot are [T][top_k].
+ *  capacity  as in switch_route (T keeps every token).
+ * SWITCH_E4M3 has the shape rules of bfloat16 (d_model, d_ff multiples of 64).
+ * Flags: SWITCH_FLAG_SIMT_FFN (CUDA cores for 16- and 8-bit experts; always so
+ * for float32 ones); others give SWITCH_ERR_UNSUPPORTED.
+ * A token with a NaN or an infinity gets a row of y and gates that are not
+ * finite; the other tokens' rows are not touched by it.  Its expert is some
+ * valid index.
+ * Errors: SWITCH_ERR_SHAPE for T > SWITCH_FEW_MAX_TOKENS, top_k, or N < top_k;
+ * SWITCH_ERR_NULL for a missing scale, SWITCH_ERR_DTYPE for a scale that the
+ * type has no use for; otherwise as switch_layer_fwd.  The workspace needs no
+ * initialisation and serves one call at a time.  Identical inputs give
+ * identical bytes. */
+#define SWITCH_FEW_MAX_TOKENS 64
+
+/* Bytes of device workspace for switch_layer_fwd_few.  Host only. */
+switch_status_t switch_few_workspace_size(const switch_dims_t *dims, int32_t top_k, size_t *bytes);
+
+switch_status_t switch_layer_fwd_few(const switch_dims_t *dims, int32_t top_k, const void *x, const float *x_scale,
+                                     const float *w_r, const float *logit_bias, const void *w_in,
+                                     const float *w_in_scale, const void *w_out, const float *w_out_scale, float *y,
+                                     int32_t *expert, float *gate, int32_t *slot, int32_t *counts, float *aux,
+                                     void *workspace, size_t workspace_bytes, switch_stream_t stream);
+
+/* ---- residual and norm before the layer ---------------------------------
+ * The layer returns y without the residual.  These calls add it, normalise
+ * the sum for the next layer, and take the gradient back:
+ *   s    = residual + delta            in float32, rounded once to residual's type
+ *   rstd = 1 / sqrt(mean_j s_j^2 + eps)
+ *   v_j  = s_j * rstd * weight_j       in float32
+ *   out  = v rounded to out_dtype; for SWITCH_E4M3: scale = max_j |v_j| / 448,
+ *          out_j = e4m3(v_j / scale)   (nearest, ties to even)
+ * A row of zeros has scale 0 and zeros; a row with a NaN or an infinity has a
+ * scale (or outputs) that are not finite, and no other row does. */
+typedef struct {
+    int64_t T;              /* rows; 0 <= T < 2^31 */
+    int32_t d_model;        /* d, 1..8192 (any; multiples of 8 are faster) */
+    int32_t residual_dtype; /* of residual and sum: SWITCH_F32 or SWITCH_BF16 */
+    int32_t delta_dtype;    /* SWITCH_F32 (a layer's y) or SWITCH_BF16; looked at with a delta only */
+    int32_t out_dtype;      /* SWITCH_F32, SWITCH_BF16 or SWITCH_E4M3 */
+    float eps;              /* >= 0, finite */
+} switch_norm_dims_t;
+
+/* residual [T, d]; delta [T, d] or NULL (then s = residual); weight [d];
+ * sum [T, d] receives s (NULL: not stored; must be NULL without a delta; may
+ * be residual itself); out [T, d]; scale [T] (SWITCH_E4M3 only, else NULL);
+ * rstd [T] or NULL.  No other overlap is allowed.  Errors: SWITCH_ERR_NULL,
+ * SWITCH_ERR_SHAPE (sizes, eps, a sum without a delta), SWITCH_ERR_DTYPE (types, a scale without
+ * SWITCH_E4M3), SWITCH_ERR_ALIGN. */
+switch_status_t switch_norm_fwd(const switch_norm_dims_t *dims, const void *residual, const void *delta,
+                                const float *weight, void *sum, void *out, float *scale, float *rstd,
+                                switch_stream_t stream);
+
+/* Bytes of device workspace for switch_norm_bwd.  Host only. */
+switch_status_t switch_norm_workspace_size(const switch_norm_dims_t *dims, size_t *bytes);
+
+/* Gradient of L through v, for dout = dL/dv [T, d] float32 (switch_layer_bwd's
+ * dx) and dsum = dL/ds [T, d] float32 from s's other uses (NULL: none):
+ *   dresidual_j = dsum_j + rstd (dout_j weight_j - s_j rstd m)
+ *                 with m = mean_j (dout_j weight_j s_j rstd)     [T, d] float32
+ *   dweight_j   = sum over rows of dout_j s_j rstd               [d]    float32
+ * dresidual is the gradient of residual and of delta alike (the roundings of s
+ * and v pass gradients unchanged).  sum [T, d] and rstd [T] are what
+ * switch_norm_fwd left (without a delta, sum is residual); out_dtype and
+ * delta_dtype are not looked at.  dresidual may be dsum or dout.  dweight is
+ * 0 when T == 0.  Deterministic. */
+switch_status_t switch_norm_bwd(const switch_norm_dims_t *dims, const void *sum, const float *weight,
+                                const float *rstd, const float *dout, const float *dsum, float *dresidual,
+                                float *dweight, void *workspace, size_t workspace_bytes, switch_stream_t stream);
+
+/* Rows in 8 bits with scales, as above: scale[r] = max_j |x[r, j]| / 448 and
+ * q[r, j] = e4m3(x[r, j] / scale[r]).  x [rows, cols] SWITCH_F32 or
+ * SWITCH_BF16; q [rows, cols] SWITCH_E4M3; scale [rows].  0 <= rows < 2^31,
+ * 1 <= cols <= 32768.  (Experts for switch_layer_fwd_few: W_in as N * F rows of
+ * d, W_out as N * d rows of F.) */
+switch_status_t switch_quantize_rows(int64_t rows, int32_t cols, int32_t dtype, const void *x, void *q, float *scale,
+                                     switch_stream_t stream);
 
 /* Routing without a workspace, for callers that cannot allocate device
  * memory at the point where they route tokens: code running under a host

@@ -14,7 +14,11 @@ place of pointers):
     switch_capacity, switch_workspace_size, switch_route, switch_dispatch,
     switch_expert_ffn, switch_combine, switch_layer_fwd, switch_check
 High level (allocate outputs and workspace with torch):
-    capacity, layer_fwd, route, dispatch, expert_ffn, combine
+    capacity, layer_fwd, layer_bwd, layer_fwd_top2, route, route_top2, router_stats
+    norm_fwd, norm_bwd      the residual's addition with its root-mean-square norm, and its gradient
+    quantize_rows           rows in 8 bits with scales
+    FewLayer, layer_fwd_few the whole layer for a few tokens (float32, bfloat16 or 8-bit experts)
+    block_fwd, block_bwd    residual and norm, then the layer
 """
 from __future__ import annotations
 
@@ -26,6 +30,8 @@ LIB_PATH = _PKG / "libswitchmoe.so"
 
 SWITCH_F32 = 0
 SWITCH_BF16 = 1
+SWITCH_E4M3 = 2
+SWITCH_FEW_MAX_TOKENS = 64
 SWITCH_FLAG_SIMT_FFN = 1
 SWITCH_FLAG_SIMT_ROUTER = 2
 SWITCH_FLAG_GEMM_1CTA = 4
@@ -46,6 +52,8 @@ EXPORTED = ("switch_capacity", "switch_workspace_size", "switch_route", "switch_
             "switch_expert_ffn",
             "switch_combine", "switch_layer_fwd", "switch_route_top2", "switch_combine_top2", "switch_layer_fwd_top2",
             "switch_layer_bwd", "switch_router_stats",
+            "switch_few_workspace_size", "switch_layer_fwd_few", "switch_norm_fwd", "switch_norm_workspace_size",
+            "switch_norm_bwd", "switch_quantize_rows",
             "switch_check", "switch_selftest_wait_timeout", "switch_check_noalloc",
             "switch_selftest_wait_timeout_noalloc", "switch_status_string",
             "switch_launch_count",
@@ -68,6 +76,15 @@ class SwitchDims(ctypes.Structure):
                 f"capacity={self.capacity}, dtype={self.dtype}, flags={self.flags})")
 
 
+class SwitchNormDims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("d_model", ctypes.c_int32), ("residual_dtype", ctypes.c_int32),
+                ("delta_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+    def __repr__(self):
+        return (f"SwitchNormDims(T={self.T}, d_model={self.d_model}, residual_dtype={self.residual_dtype}, "
+                f"delta_dtype={self.delta_dtype}, out_dtype={self.out_dtype}, eps={self.eps})")
+
+
 _lib = None
 
 
@@ -81,6 +98,7 @@ def lib() -> ctypes.CDLL:
     L = ctypes.CDLL(str(LIB_PATH))
     P, S = ctypes.c_void_p, ctypes.c_size_t
     D = ctypes.POINTER(SwitchDims)
+    ND = ctypes.POINTER(SwitchNormDims)
     I = ctypes.c_int
     sig = {
         "switch_capacity": (ctypes.c_int64, [ctypes.c_int64, ctypes.c_int32, ctypes.c_double]),
@@ -96,6 +114,12 @@ def lib() -> ctypes.CDLL:
         "switch_layer_fwd_top2": (I, [D, P, P, P, P, P, P, P, P, P, P, P, P, S, P]),
         "switch_layer_bwd": (I, [D, P, P, P, P, P, P, P, P, P, ctypes.c_float, P, P, P, P, P, P, S, P]),
         "switch_router_stats": (I, [D, P, P, S, P, P]),
+        "switch_few_workspace_size": (I, [D, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),
+        "switch_layer_fwd_few": (I, [D, ctypes.c_int32] + [P] * 15 + [S, P]),
+        "switch_norm_fwd": (I, [ND, P, P, P, P, P, P, P, P]),
+        "switch_norm_workspace_size": (I, [ND, ctypes.POINTER(ctypes.c_size_t)]),
+        "switch_norm_bwd": (I, [ND, P, P, P, P, P, P, P, P, S, P]),
+        "switch_quantize_rows": (I, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, P, P, P, P]),
         "switch_check": (I, [P, S, P]),
         "switch_selftest_wait_timeout": (I, [P, S, P]),
         "switch_check_noalloc": (I, [P]),
@@ -251,6 +275,45 @@ def switch_router_stats(d, counts, workspace, stats, stream=None):
     _ok(lib().switch_router_stats(ctypes.byref(d), _ptr(counts), _ptr(workspace),
                                   workspace.numel() * workspace.element_size(), _ptr(stats),
                                   _stream(stream, workspace)), "switch_router_stats")
+
+
+def switch_few_workspace_size(d: SwitchDims, top_k: int) -> int:
+    out = ctypes.c_size_t(0)
+    _ok(lib().switch_few_workspace_size(ctypes.byref(d), int(top_k), ctypes.byref(out)), "switch_few_workspace_size")
+    return int(out.value)
+
+
+def switch_layer_fwd_few(d, top_k, x, x_scale, w_r, logit_bias, w_in, w_in_scale, w_out, w_out_scale, y, expert, gate,
+                         slot, counts, aux, workspace, stream=None):
+    _ok(lib().switch_layer_fwd_few(ctypes.byref(d), int(top_k), _ptr(x), _ptr(x_scale), _ptr(w_r), _ptr(logit_bias),
+                                   _ptr(w_in), _ptr(w_in_scale), _ptr(w_out), _ptr(w_out_scale), _ptr(y),
+                                   _ptr(expert), _ptr(gate), _ptr(slot), _ptr(counts), _ptr(aux), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream(stream, workspace)),
+        "switch_layer_fwd_few")
+
+
+def switch_norm_fwd(d, residual, delta, weight, sum, out, scale, rstd, stream=None):
+    _ok(lib().switch_norm_fwd(ctypes.byref(d), _ptr(residual), _ptr(delta), _ptr(weight), _ptr(sum), _ptr(out),
+                              _ptr(scale), _ptr(rstd), _stream(stream, out)), "switch_norm_fwd")
+
+
+def switch_norm_workspace_size(d: SwitchNormDims) -> int:
+    out = ctypes.c_size_t(0)
+    _ok(lib().switch_norm_workspace_size(ctypes.byref(d), ctypes.byref(out)), "switch_norm_workspace_size")
+    return int(out.value)
+
+
+def switch_norm_bwd(d, sum, weight, rstd, dout, dsum, dresidual, dweight, workspace, stream=None):
+    _ok(lib().switch_norm_bwd(ctypes.byref(d), _ptr(sum), _ptr(weight), _ptr(rstd), _ptr(dout), _ptr(dsum),
+                              _ptr(dresidual), _ptr(dweight), _ptr(workspace),
+                              workspace.numel() * workspace.element_size(), _stream(stream, workspace)),
+        "switch_norm_bwd")
+
+
+def switch_quantize_rows(rows, cols, dtype, x, q, scale, stream=None):
+    code = dtype if isinstance(dtype, int) else dtype_code(dtype)
+    _ok(lib().switch_quantize_rows(int(rows), int(cols), code, _ptr(x), _ptr(q), _ptr(scale), _stream(stream, q)),
+        "switch_quantize_rows")
 
 
 def switch_check(workspace, stream=None) -> int:
@@ -456,3 +519,284 @@ def router_stats(result: dict, T: int, d_model: int, d_ff: int, dtype, stream=No
     stats = torch.empty(4, dtype=torch.float32, device=counts.device)
     switch_router_stats(d, counts, result["workspace"], stats, stream)
     return stats
+
+
+# ---------------------------------------------------------------------------
+# residual + norm, 8-bit rows, the layer for a few tokens
+# ---------------------------------------------------------------------------
+def _code(dtype) -> int:
+    """dtype_code with the 8-bit type (which only the calls below take)."""
+    import torch
+    return SWITCH_E4M3 if dtype == torch.float8_e4m3fn else dtype_code(dtype)
+
+
+def _want(name, t, shape, dtypes, device):
+    """Checks an argument and returns its pointer (None for None)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return _ptr(t)
+
+
+class _Result(dict):
+    """A result that a later call of the same sizes may write into again (out=)."""
+    __slots__ = ("key",)
+
+
+def _result(out, key, make):
+    """`out` when it came from a call with the same `key`, else new outputs (out=None) or an error."""
+    if out is None:
+        out = _Result(make())
+        out.key = key
+    elif not isinstance(out, _Result) or out.key != key:
+        raise ValueError("out must be the result of an earlier call of the same function, sizes, types and device")
+    return out
+
+
+def _launch(fn, where, device, *args):
+    """Calls the C function on the current stream of `device`, which is made current meanwhile."""
+    import torch
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status != 0:
+        raise SwitchError(status, where)
+
+
+def _under(stream, device):
+    """Makes `stream` (a torch stream or a cudaStream_t) the current one, so that what is allocated meanwhile is
+    ordered on the stream that it is used on."""
+    import torch
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
+
+
+def _rows(name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, columns], got {list(t.shape)}")
+    if not t.is_cuda:
+        raise TypeError("switch_moe tensors must be CUDA tensors")
+    return t.shape[0], t.shape[1], t.device
+
+
+def norm_fwd(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None, inplace: bool = False, out=None,
+             stream=None):
+    """s = residual + delta, rounded to residual's type, and out = s / rms(s) * weight (switch_norm_fwd).
+
+    residual [T, d] float32 or bfloat16; delta [T, d] float32 or bfloat16 (a layer's y), or None for s = residual;
+    weight [d] float32; out_dtype float32, bfloat16 or float8_e4m3fn (default: residual's).  Returns a dict with
+    sum (None without a delta; residual itself with ``inplace``), out, scale ([T], 8-bit outputs only) and rstd [T].
+    ``out`` takes the result of an earlier call of the same sizes, which is overwritten."""
+    import torch
+    T, dm, dev = _rows("residual", residual)
+    if stream is not None:
+        with _under(stream, dev):
+            return norm_fwd(residual, weight, delta, eps, out_dtype, inplace, out)
+    out_dtype = residual.dtype if out_dtype is None else out_dtype
+    e4m3 = out_dtype == torch.float8_e4m3fn
+    halves = (torch.float32, torch.bfloat16)
+    pr = _want("residual", residual, (T, dm), halves, dev)
+    pd = _want("delta", delta, (T, dm), halves, dev)
+    pw = _want("weight", weight, (dm,), (torch.float32,), dev)
+    stored = delta is not None and not inplace
+
+    def make():
+        return dict(sum=torch.empty_like(residual) if stored else None,
+                    out=torch.empty(T, dm, dtype=out_dtype, device=dev),
+                    scale=torch.empty(T, dtype=torch.float32, device=dev) if e4m3 else None,
+                    rstd=torch.empty(T, dtype=torch.float32, device=dev))
+
+    out = _result(out, ("norm_fwd", T, dm, residual.dtype, out_dtype, stored, dev), make)
+    if delta is not None and inplace:
+        out["sum"] = residual
+    d = SwitchNormDims(T, dm, dtype_code(residual.dtype), SWITCH_F32 if delta is None else dtype_code(delta.dtype),
+                       _code(out_dtype), eps)
+    _launch(lib().switch_norm_fwd, "switch_norm_fwd", dev, ctypes.byref(d), pr, pd, pw, _ptr(out["sum"]),
+            _ptr(out["out"]), _ptr(out["scale"]), _ptr(out["rstd"]))
+    return out
+
+
+def norm_bwd(sum, weight, rstd, dout, dsum=None, out=None, stream=None):
+    """Gradient of norm_fwd (switch_norm_bwd): from dout [T, d] float32 (the gradient of its out) and dsum [T, d]
+    float32 (the gradient of its sum from elsewhere, or None), dresidual [T, d] (of residual and of delta alike) and
+    dweight [d], float32.  sum is norm_fwd's sum, or residual where there was no delta."""
+    import torch
+    T, dm, dev = _rows("sum", sum)
+    if stream is not None:
+        with _under(stream, dev):
+            return norm_bwd(sum, weight, rstd, dout, dsum, out)
+    f32 = (torch.float32,)
+    ps = _want("sum", sum, (T, dm), (torch.float32, torch.bfloat16), dev)
+    pw, pr = _want("weight", weight, (dm,), f32, dev), _want("rstd", rstd, (T,), f32, dev)
+    pg, pu = _want("dout", dout, (T, dm), f32, dev), _want("dsum", dsum, (T, dm), f32, dev)
+    out = _result(out, ("norm_bwd", T, dm, dev), lambda: dict(
+        dresidual=torch.empty(T, dm, dtype=torch.float32, device=dev),
+        dweight=torch.empty(dm, dtype=torch.float32, device=dev)))
+    d = SwitchNormDims(T, dm, dtype_code(sum.dtype), SWITCH_F32, SWITCH_F32, 0.0)
+    size = switch_norm_workspace_size(d)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    _launch(lib().switch_norm_bwd, "switch_norm_bwd", dev, ctypes.byref(d), ps, pw, pr, pg, pu,
+            _ptr(out["dresidual"]), _ptr(out["dweight"]), ws.data_ptr(), size)
+    return out
+
+
+def quantize_rows(x, out=None, stream=None):
+    """x [..., cols] float32 or bfloat16 in 8 bits (switch_quantize_rows): a dict with q (float8_e4m3fn, x's shape)
+    and scale (float32, x's shape without the last dimension); x is about q * scale."""
+    import torch
+    if not x.is_cuda:
+        raise TypeError("switch_moe tensors must be CUDA tensors")
+    if x.dim() < 1:
+        raise ValueError("x must have rows")
+    dev, cols = x.device, x.shape[-1]
+    if stream is not None:
+        with _under(stream, dev):
+            return quantize_rows(x, out)
+    rows = 1
+    for n in x.shape[:-1]:
+        rows *= n
+    px = _want("x", x, x.shape, (torch.float32, torch.bfloat16), dev)
+    out = _result(out, ("quantize_rows", tuple(x.shape), dev), lambda: dict(
+        q=torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev),
+        scale=torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)))
+    _launch(lib().switch_quantize_rows, "switch_quantize_rows", dev, rows, cols, dtype_code(x.dtype), px,
+            _ptr(out["q"]), _ptr(out["scale"]))
+    return out
+
+
+class FewLayer:
+    """The layer for up to 64 tokens over one set of weights (switch_layer_fwd_few): the handle that a serving
+    program keeps.  w_r [N, d] float32; w_in [N, F, d] and w_out [N, d, F] float32, bfloat16 or float8_e4m3fn, the
+    last with w_in_scale [N, F] and w_out_scale [N, d] (quantize_rows makes both).  ``capacity`` None keeps every
+    token.  The tensors are held and read at each call; calls may run on several streams at once (each has a
+    workspace of its own unless it is given one)."""
+
+    def __init__(self, w_r, w_in, w_out, top_k: int = 1, capacity=None, capacity_factor=None, logit_bias=None,
+                 w_in_scale=None, w_out_scale=None, flags: int = 0):
+        import torch
+        if w_in.dim() != 3:
+            raise ValueError("w_in must be [N, d_ff, d_model]")
+        N, F, dm = w_in.shape
+        dev = w_in.device
+        e4m3 = w_in.dtype == torch.float8_e4m3fn
+        if e4m3 != (w_in_scale is not None) or e4m3 != (w_out_scale is not None):
+            raise ValueError("float8_e4m3fn experts, and they only, have w_in_scale and w_out_scale")
+        f32 = (torch.float32,)
+        _want("w_in", w_in, (N, F, dm), (torch.float32, torch.bfloat16, torch.float8_e4m3fn), dev)
+        _want("w_out", w_out, (N, dm, F), (w_in.dtype,), dev)
+        _want("w_r", w_r, (N, dm), f32, dev)
+        _want("logit_bias", logit_bias, (N,), f32, dev)
+        _want("w_in_scale", w_in_scale, (N, F), f32, dev)
+        _want("w_out_scale", w_out_scale, (N, dm), f32, dev)
+        if capacity is not None and capacity_factor is not None:
+            raise ValueError("give capacity or capacity_factor, not both")
+        self.w_r, self.w_in, self.w_out, self.logit_bias = w_r, w_in, w_out, logit_bias
+        self.w_in_scale, self.w_out_scale = w_in_scale, w_out_scale
+        self.top_k, self.capacity, self.capacity_factor, self.flags = int(top_k), capacity, capacity_factor, int(flags)
+        self.num_experts, self.d_ff, self.d_model, self.device, self.dtype = N, F, dm, dev, w_in.dtype
+        self._sizes = {}
+        self._dims(1)  # refuses sizes that no call could run with
+
+    def _dims(self, T):
+        """(dims, workspace bytes) of calls with T tokens."""
+        got = self._sizes.get(T)
+        if got is None:
+            if self.capacity is not None:
+                C = int(self.capacity)
+            elif self.capacity_factor is not None:
+                C = _resolve_capacity(T, self.num_experts, None, self.capacity_factor)
+            else:
+                C = max(1, T)
+            d = dims(T, self.d_model, self.d_ff, self.num_experts, C, _code(self.dtype), self.flags)
+            got = self._sizes[T] = (d, switch_few_workspace_size(d, self.top_k))
+        return got
+
+    def __call__(self, x, x_scale=None, out=None, ws=None, stream=None):
+        """x [T, d] of the experts' type (8-bit experts: bfloat16, or float8_e4m3fn with x_scale [T] float32).
+        Returns a dict with y [T, d] float32 (no residual), aux, expert / gate / slot ([T], or [T, 2] with top_k 2)
+        and counts.  ``out`` takes the result of an earlier call with as many tokens, which is overwritten."""
+        import torch
+        dev = self.device
+        if stream is not None:
+            with _under(stream, dev):
+                return self(x, x_scale, out, ws)
+        if x.dim() != 2:
+            raise ValueError(f"x must be [T, {self.d_model}], got {list(x.shape)}")
+        T, k = x.shape[0], self.top_k
+        if self.dtype != torch.float8_e4m3fn:
+            if x_scale is not None:
+                raise ValueError("x_scale goes with float8_e4m3fn experts and x")
+            types = (self.dtype,)
+        else:
+            types = (torch.bfloat16,) if x_scale is None else (torch.float8_e4m3fn,)
+        px = _want("x", x, (T, self.d_model), types, dev)
+        pxs = _want("x_scale", x_scale, (T,), (torch.float32,), dev)
+        d, size = self._dims(T)
+
+        def make():
+            shape = (T,) if k == 1 else (T, k)
+            return dict(y=torch.empty(T, self.d_model, dtype=torch.float32, device=dev),
+                        expert=torch.empty(shape, dtype=torch.int32, device=dev),
+                        gate=torch.empty(shape, dtype=torch.float32, device=dev),
+                        slot=torch.empty(shape, dtype=torch.int32, device=dev),
+                        counts=torch.empty(self.num_experts, dtype=torch.int32, device=dev),
+                        aux=torch.empty(1, dtype=torch.float32, device=dev))
+
+        out = _result(out, ("few", T, k, self.d_model, self.num_experts, dev), make)
+        if ws is None:
+            ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        bias, si, so = self.logit_bias, self.w_in_scale, self.w_out_scale
+        _launch(lib().switch_layer_fwd_few, "switch_layer_fwd_few", dev, ctypes.byref(d), k, px, pxs,
+                self.w_r.data_ptr(), None if bias is None else bias.data_ptr(), self.w_in.data_ptr(),
+                None if si is None else si.data_ptr(), self.w_out.data_ptr(), None if so is None else so.data_ptr(),
+                out["y"].data_ptr(), out["expert"].data_ptr(), out["gate"].data_ptr(), out["slot"].data_ptr(),
+                out["counts"].data_ptr(), out["aux"].data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+        out["capacity"], out["flags"], out["workspace"] = d.capacity, d.flags, ws
+        return out
+
+
+def layer_fwd_few(x, w_r, w_in, w_out, top_k: int = 1, capacity=None, capacity_factor=None, logit_bias=None,
+                  x_scale=None, w_in_scale=None, w_out_scale=None, flags: int = 0, ws=None, out=None, stream=None):
+    """layer_fwd / layer_fwd_top2 for up to 64 tokens (see FewLayer, which saves the checks of the weights)."""
+    return FewLayer(w_r, w_in, w_out, top_k, capacity, capacity_factor, logit_bias, w_in_scale, w_out_scale, flags)(
+        x, x_scale, out, ws, stream)
+
+
+def block_fwd(residual, norm_weight, w_r, w_in, w_out, delta=None, eps: float = 1e-6, top_k: int = 1, capacity=None,
+              capacity_factor=None, logit_bias=None, w_in_scale=None, w_out_scale=None, flags: int = 0, stream=None):
+    """One pre-norm block: s = residual + delta, x = s / rms(s) * norm_weight, y = layer(x); the caller adds y as
+    the next block's delta.  Up to 64 tokens outside of training go through switch_layer_fwd_few (8-bit experts
+    always do, with x in 8 bits), others through switch_layer_fwd / switch_layer_fwd_top2.  Returns the layer's
+    dict with sum (residual where there is no delta), x, x_scale and rstd besides."""
+    import torch
+    few = w_in.dtype == torch.float8_e4m3fn or (residual.shape[0] <= SWITCH_FEW_MAX_TOKENS
+                                                and (flags & ~SWITCH_FLAG_SIMT_FFN) == 0)
+    if not few and top_k not in (1, 2):
+        raise ValueError("top_k must be 1 or 2")
+    n = norm_fwd(residual, norm_weight, delta=delta, eps=eps, out_dtype=w_in.dtype, stream=stream)
+    x = n["out"]
+    if few:
+        if capacity is None and capacity_factor is None:
+            raise ValueError("give capacity or capacity_factor")
+        r = layer_fwd_few(x, w_r, w_in, w_out, top_k, capacity, capacity_factor, logit_bias, n["scale"], w_in_scale,
+                          w_out_scale, flags, stream=stream)
+    else:
+        r = (layer_fwd if top_k == 1 else layer_fwd_top2)(x, w_r, w_in, w_out, capacity, capacity_factor, logit_bias,
+                                                          flags, stream=stream)
+    return dict(r, sum=residual if delta is None else n["sum"], x=x, x_scale=n["scale"], rstd=n["rstd"])
+
+
+def block_bwd(fwd: dict, norm_weight, w_r, w_in, w_out, dy, dsum=None, g_aux: float = 0.0, logit_bias=None,
+              stream=None):
+    """Gradients of sum(y * dy) + sum(s * dsum) + g_aux * aux after ``block_fwd(..., flags=SWITCH_FLAG_TRAINING)``:
+    layer_bwd's dw_r, dbias, dw_in, dw_out, with dresidual (of residual and delta alike) and dnorm_weight, float32."""
+    g = layer_bwd(fwd, fwd["x"], w_r, w_in, w_out, dy, g_aux, logit_bias, stream)
+    n = norm_bwd(fwd["sum"], norm_weight, fwd["rstd"], g.pop("dx"), dsum=dsum, stream=stream)
+    return dict(g, dresidual=n["dresidual"], dnorm_weight=n["dweight"])

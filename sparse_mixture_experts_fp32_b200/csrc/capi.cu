@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "few.cuh"
 #include "internal.h"
 
 namespace switchmoe {
@@ -136,6 +137,23 @@ switch_status_t check_dims(const switch_dims_t *d) {
     if ((int64_t)d->num_experts * d->capacity > INT32_MAX) return SWITCH_ERR_SHAPE;
     if (d->dtype == SWITCH_BF16 && (d->d_model % 64 != 0 || d->d_ff % 64 != 0)) return SWITCH_ERR_SHAPE;
     return SWITCH_OK;
+}
+
+switch_status_t check_few_dims(const switch_dims_t *d, int32_t top_k) {
+    if (!d) return SWITCH_ERR_NULL;
+    switch_dims_t as16 = *d;  // 8-bit experts have the shape rules of 16-bit ones
+    if (d->dtype == SWITCH_E4M3) as16.dtype = SWITCH_BF16;
+    const switch_status_t s = check_dims(&as16);
+    if (s != SWITCH_OK) return s;
+    if (d->T > SWITCH_FEW_MAX_TOKENS || top_k < 1 || top_k > 2 || d->num_experts < top_k) return SWITCH_ERR_SHAPE;
+    return (d->flags & ~SWITCH_FLAG_SIMT_FFN) ? SWITCH_ERR_UNSUPPORTED : SWITCH_OK;
+}
+
+switch_status_t check_norm_dims(const switch_norm_dims_t *d) {
+    if (!d) return SWITCH_ERR_NULL;
+    if (d->residual_dtype != SWITCH_F32 && d->residual_dtype != SWITCH_BF16) return SWITCH_ERR_DTYPE;
+    if (d->T < 0 || d->T > INT32_MAX || d->d_model < 1 || d->d_model > 8192) return SWITCH_ERR_SHAPE;
+    return d->eps >= 0.f && std::isfinite(d->eps) ? SWITCH_OK : SWITCH_ERR_SHAPE;
 }
 
 // Pointers that must be present; all of them must also be 16-byte aligned.
@@ -472,6 +490,94 @@ switch_status_t switch_layer_bwd(const switch_dims_t *dims, const void *x, const
                                       dbias, dw_in, dw_out, ws, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+switch_status_t switch_few_workspace_size(const switch_dims_t *dims, int32_t top_k, size_t *bytes) {
+    if (!bytes) return SWITCH_ERR_NULL;
+    const switch_status_t s = check_few_dims(dims, top_k);
+    if (s != SWITCH_OK) return s;
+    *bytes = few_workspace_bytes(*dims, top_k);
+    return SWITCH_OK;
+}
+
+switch_status_t switch_layer_fwd_few(const switch_dims_t *dims, int32_t top_k, const void *x, const float *x_scale,
+                                     const float *w_r, const float *logit_bias, const void *w_in,
+                                     const float *w_in_scale, const void *w_out, const float *w_out_scale, float *y,
+                                     int32_t *expert, float *gate, int32_t *slot, int32_t *counts, float *aux,
+                                     void *workspace, size_t workspace_bytes_given, switch_stream_t stream) {
+    switch_status_t s = check_few_dims(dims, top_k);
+    if (s != SWITCH_OK) return s;
+    const bool e4m3 = dims->dtype == SWITCH_E4M3, has_tokens = dims->T > 0;
+    if (!e4m3 && (x_scale || w_in_scale || w_out_scale)) return SWITCH_ERR_DTYPE;
+    s = check_ptrs({w_r, w_in, w_out, counts, aux, workspace, has_tokens ? x : w_r, has_tokens ? (const void *)y : w_r,
+                    has_tokens ? (const void *)expert : w_r, has_tokens ? (const void *)gate : w_r,
+                    has_tokens ? (const void *)slot : w_r, e4m3 ? w_in_scale : w_r, e4m3 ? w_out_scale : w_r},
+                   {logit_bias, x, y, expert, gate, slot, x_scale});
+    if (s != SWITCH_OK) return s;
+    if (workspace_bytes_given < few_workspace_bytes(*dims, top_k)) return SWITCH_ERR_WORKSPACE;
+    if ((s = check_device()) != SWITCH_OK) return s;
+    FewArgs a{};
+    a.T = (int)dims->T, a.d = dims->d_model, a.F = dims->d_ff, a.N = dims->num_experts, a.C = dims->capacity;
+    a.k = top_k;
+    a.x = x, a.x_scale = x_scale, a.w_r = w_r, a.bias = logit_bias;
+    a.w_in = w_in, a.w_out = w_out, a.w_in_scale = w_in_scale, a.w_out_scale = w_out_scale;
+    a.y = y, a.gate = gate, a.aux = aux, a.expert = expert, a.slot = slot, a.counts = counts;
+    const int x_dtype = e4m3 ? (x_scale ? SWITCH_E4M3 : SWITCH_BF16) : dims->dtype;
+    return from_cuda(launch_layer_few(*dims, x_dtype, a, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+switch_status_t switch_norm_fwd(const switch_norm_dims_t *dims, const void *residual, const void *delta,
+                                const float *weight, void *sum, void *out, float *scale, float *rstd,
+                                switch_stream_t stream) {
+    switch_status_t s = check_norm_dims(dims);
+    if (s != SWITCH_OK) return s;
+    if (dims->out_dtype < SWITCH_F32 || dims->out_dtype > SWITCH_E4M3) return SWITCH_ERR_DTYPE;
+    if (delta && dims->delta_dtype != SWITCH_F32 && dims->delta_dtype != SWITCH_BF16) return SWITCH_ERR_DTYPE;
+    const bool e4m3 = dims->out_dtype == SWITCH_E4M3, has_rows = dims->T > 0;
+    if (scale && !e4m3) return SWITCH_ERR_DTYPE;
+    if (sum && !delta) return SWITCH_ERR_SHAPE;
+    s = check_ptrs({weight, has_rows ? residual : weight, has_rows ? out : weight,
+                    has_rows && e4m3 ? (const void *)scale : weight},
+                   {residual, delta, sum, out, scale, rstd});
+    if (s != SWITCH_OK) return s;
+    if ((s = check_device()) != SWITCH_OK) return s;
+    return from_cuda(launch_norm_fwd(*dims, residual, delta, weight, sum, out, scale, rstd,
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+switch_status_t switch_norm_workspace_size(const switch_norm_dims_t *dims, size_t *bytes) {
+    if (!bytes) return SWITCH_ERR_NULL;
+    const switch_status_t s = check_norm_dims(dims);
+    if (s != SWITCH_OK) return s;
+    *bytes = norm_workspace_bytes(*dims);
+    return SWITCH_OK;
+}
+
+switch_status_t switch_norm_bwd(const switch_norm_dims_t *dims, const void *sum, const float *weight,
+                                const float *rstd, const float *dout, const float *dsum, float *dresidual,
+                                float *dweight, void *workspace, size_t workspace_bytes_given,
+                                switch_stream_t stream) {
+    switch_status_t s = check_norm_dims(dims);
+    if (s != SWITCH_OK) return s;
+    const bool has_rows = dims->T > 0;
+    s = check_ptrs({weight, dweight, workspace, has_rows ? sum : weight, has_rows ? (const void *)rstd : weight,
+                    has_rows ? (const void *)dout : weight, has_rows ? (const void *)dresidual : weight},
+                   {sum, rstd, dout, dsum, dresidual});
+    if (s != SWITCH_OK) return s;
+    if (workspace_bytes_given < norm_workspace_bytes(*dims)) return SWITCH_ERR_WORKSPACE;
+    if ((s = check_device()) != SWITCH_OK) return s;
+    return from_cuda(launch_norm_bwd(*dims, sum, weight, rstd, dout, dsum, dresidual, dweight, workspace,
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+switch_status_t switch_quantize_rows(int64_t rows, int32_t cols, int32_t dtype, const void *x, void *q, float *scale,
+                                     switch_stream_t stream) {
+    if (dtype != SWITCH_F32 && dtype != SWITCH_BF16) return SWITCH_ERR_DTYPE;
+    if (rows < 0 || rows > INT32_MAX || cols < 1 || cols > 32768) return SWITCH_ERR_SHAPE;
+    switch_status_t s;
+    if (rows > 0 && (s = check_ptrs({x, q, scale}, {})) != SWITCH_OK) return s;
+    if ((s = check_device()) != SWITCH_OK) return s;
+    return from_cuda(launch_quantize_rows(rows, cols, dtype, x, q, scale, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 switch_status_t switch_check(void *workspace, size_t workspace_bytes_given, switch_stream_t stream) {
     if (!workspace) return SWITCH_ERR_NULL;
     if (workspace_bytes_given < sizeof(DeviceStatus)) return SWITCH_ERR_WORKSPACE;
@@ -590,6 +696,13 @@ const char *switch_kernel_name(int32_t id) {
         case K_BWD_ROUTER_TC_DX: return "bwd_router_tc_dx";
         case K_BWD_ROUTER_TC_DW: return "bwd_router_tc_dw";
         case K_BWD_ZERO_TAILS: return "bwd_zero_tails";
+        case K_NORM_FWD: return "norm_fwd";
+        case K_NORM_BWD: return "norm_bwd";
+        case K_NORM_DWEIGHT: return "norm_dweight";
+        case K_QUANTIZE_ROWS: return "quantize_rows";
+        case K_FEW_ROUTER: return "few_router";
+        case K_FEW_EXPERTS_SIMT: return "few_experts_simt";
+        case K_FEW_EXPERTS_TC: return "few_experts_tc";
     }
     return "?";
 }

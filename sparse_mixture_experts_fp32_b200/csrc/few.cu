@@ -1,0 +1,390 @@
+// The whole layer for a few tokens (a decoding step): two kernels.
+//
+//   few_router   logits = W_r x (+ b), float32
+//   few_experts  softmax, top-1 or top-2, slots, then for the experts that
+//                were reached h = ReLU(W_in x) and o = W_out h, and
+//                y = sum over the kept choices of gate * o
+//
+// With few tokens the layer is bound by reading the weights of the experts
+// that the tokens reach (2 d F elements each) once.  So the second kernel is
+// one persistent launch over both products: blocks claim items of work in
+// order from a counter, all items of the first product before any of the
+// second, and an item of the second product waits until the first product of
+// its expert is complete (a counter per group).  Only running blocks hold
+// claims and items of the first product wait for nothing, so the wait ends
+// whatever else occupies the GPU; it is bounded all the same.  The block that
+// finishes the last item of a tile of output rows forms y there, in a fixed
+// order: no sum depends on the order in which blocks finish.
+//
+// This file: the router and the CUDA-core form (float32 experts, and any
+// with SWITCH_FLAG_SIMT_FFN).
+#include <type_traits>
+
+#include "few.cuh"
+
+namespace switchmoe {
+namespace {
+
+// ---------------------------------------------------------------------------
+// element loads
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void e4m3x4_to_float(uint32_t w, float *v) {
+    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+    const float2 a = __half22float2(__half2(lo)), b = __half22float2(__half2(hi));
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+}
+
+// V consecutive elements (V * sizeof(T) bytes aligned to their size, 16 at most)
+template <typename T, int V>
+__device__ __forceinline__ void load_elems(const T *p, float (&v)[V]) {
+    if constexpr (V == 1) {
+        v[0] = Elem<T>::load(p, 0);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const float4 a = reinterpret_cast<const float4 *>(p)[i];
+            v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
+        }
+    } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const uint2 a = reinterpret_cast<const uint2 *>(p)[i];
+            v[4 * i] = __uint_as_float(a.x << 16), v[4 * i + 1] = __uint_as_float(a.x & 0xffff0000u);
+            v[4 * i + 2] = __uint_as_float(a.y << 16), v[4 * i + 3] = __uint_as_float(a.y & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) e4m3x4_to_float(reinterpret_cast<const uint32_t *>(p)[i], v + 4 * i);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// router
+// ---------------------------------------------------------------------------
+constexpr int kRouterThreads = 256;
+
+// Block (i, j): the logits of TE experts for TT tokens, the dot products
+// spread over the block's threads, V elements each; sums in a fixed order.
+template <typename X, int V, int TE, int TT>
+__global__ void __launch_bounds__(kRouterThreads)
+    few_router_kernel(const FewArgs p, int zero_ints, int want_xmax) {
+    __shared__ float red[kRouterThreads / 32][TE * TT];
+    __shared__ uint32_t big[kRouterThreads / 32][TT];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int e0 = blockIdx.x * TE, t0 = blockIdx.y * TT;
+    pdl_launch_dependents();
+    {  // the second kernel's counters and maxima, and the status word
+        const int blocks = gridDim.x * gridDim.y, me = blockIdx.y * gridDim.x + blockIdx.x;
+        int32_t *z = reinterpret_cast<int32_t *>(p.ctr);
+        for (int i = me * kRouterThreads + tid; i < zero_ints; i += blocks * kRouterThreads) z[i] = 0;
+        if (me == 0 && tid < (int)(sizeof(DeviceStatus) / 4)) reinterpret_cast<int32_t *>(p.status)[tid] = 0;
+    }
+    const X *x = static_cast<const X *>(p.x);
+    const float *w[TE];
+    const X *xr[TT];
+#pragma unroll
+    for (int e = 0; e < TE; ++e) w[e] = p.w_r + (int64_t)min(e0 + e, p.N - 1) * p.d;
+#pragma unroll
+    for (int t = 0; t < TT; ++t) xr[t] = x + (int64_t)min(t0 + t, p.T - 1) * p.d;
+    float acc[TE][TT];
+    uint32_t top[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        top[t] = 0;
+#pragma unroll
+        for (int e = 0; e < TE; ++e) acc[e][t] = 0.f;
+    }
+    for (int j = tid * V; j < p.d; j += kRouterThreads * V) {
+        float wv[TE][V];
+#pragma unroll
+        for (int e = 0; e < TE; ++e) load_elems<float, V>(w[e] + j, wv[e]);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            float xv[V];
+            load_elems<X, V>(xr[t] + j, xv);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                top[t] = max(top[t], __float_as_uint(xv[i]) & 0x7fffffffu);
+#pragma unroll
+                for (int e = 0; e < TE; ++e) acc[e][t] = fmaf(wv[e][i], xv[i], acc[e][t]);
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < TE; ++e)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            float a = acc[e][t];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+            if (lane == 0) red[warp][e * TT + t] = a;
+        }
+    if (want_xmax && blockIdx.x == 0) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const uint32_t b = __reduce_max_sync(0xffffffffu, top[t]);
+            if (lane == 0) big[warp][t] = b;
+        }
+    }
+    __syncthreads();
+    if (tid < TE * TT) {
+        const int e = e0 + tid / TT, t = t0 + tid % TT;
+        if (e < p.N && t < p.T) {
+            float a = 0.f;
+#pragma unroll
+            for (int w8 = 0; w8 < kRouterThreads / 32; ++w8) a += red[w8][tid];
+            if (p.x_scale != nullptr) a *= p.x_scale[t];
+            if (p.bias != nullptr) a += p.bias[e];
+            p.logits[(int64_t)t * p.N + e] = a;
+        }
+    }
+    if (want_xmax && blockIdx.x == 0 && tid < TT && t0 + tid < p.T) {
+        uint32_t b = 0;
+        for (int w8 = 0; w8 < kRouterThreads / 32; ++w8) b = max(b, big[w8][tid]);
+        p.xmax[t0 + tid] = b;
+    }
+}
+
+template <typename X, int V>
+void router_typed(const FewArgs &p, int zero_ints, int want_xmax, cudaStream_t stream) {
+    // one expert per block for the most blocks in flight; with many blocks four, so that a row of x serves four
+    if (p.T == 1) {
+        few_router_kernel<X, V, 1, 1><<<dim3(p.N, 1), kRouterThreads, 0, stream>>>(p, zero_ints, want_xmax);
+    } else if (p.N * ((p.T + 7) / 8) <= 592) {
+        few_router_kernel<X, V, 1, 8><<<dim3(p.N, (p.T + 7) / 8), kRouterThreads, 0, stream>>>(p, zero_ints, want_xmax);
+    } else {
+        few_router_kernel<X, V, 4, 8>
+            <<<dim3((p.N + 3) / 4, (p.T + 7) / 8), kRouterThreads, 0, stream>>>(p, zero_ints, want_xmax);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// experts on CUDA cores
+// ---------------------------------------------------------------------------
+constexpr int kSimtThreads = 256;
+constexpr int kSimtWarps = kSimtThreads / 32;
+constexpr int kSimtRows = 8;    // weight rows of an item
+constexpr int kSimtTokens = 8;  // tokens of a group
+
+struct SimtShared {
+    FewPlan plan;
+    float red[kSimtWarps][kSimtRows * kSimtTokens];
+    int item, go, last;
+};
+
+// part[r][j] = sum_k w[r][k] in[j][k] over this warp's share of k, for
+// kSimtRows rows of weights and m tokens, reduced over the warp's lanes.
+template <typename W, typename X, int V>
+__device__ __forceinline__ void simt_dots(const W *w, int64_t rows_left, int K, const X *const *in, int m, int warp,
+                                          int lane, float *red) {
+    float acc[kSimtRows][kSimtTokens];
+#pragma unroll
+    for (int r = 0; r < kSimtRows; ++r)
+#pragma unroll
+        for (int j = 0; j < kSimtTokens; ++j) acc[r][j] = 0.f;
+    const W *wr[kSimtRows];
+#pragma unroll
+    for (int r = 0; r < kSimtRows; ++r) wr[r] = w + (r < rows_left ? r : rows_left - 1) * (int64_t)K;
+    for (int k = (warp * 32 + lane) * V; k < K; k += kSimtThreads * V) {
+        float wv[kSimtRows][V];
+#pragma unroll
+        for (int r = 0; r < kSimtRows; ++r) load_elems<W, V>(wr[r] + k, wv[r]);
+#pragma unroll
+        for (int j = 0; j < kSimtTokens; ++j) {
+            if (j < m) {
+                float xv[V];
+                load_elems<X, V>(in[j] + k, xv);
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int r = 0; r < kSimtRows; ++r) acc[r][j] = fmaf(wv[r][i], xv[i], acc[r][j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kSimtTokens; ++j) {
+        if (j < m) {
+#pragma unroll
+            for (int r = 0; r < kSimtRows; ++r) {
+                float a = acc[r][j];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+                if (lane == 0) red[r * kSimtTokens + j] = a;
+            }
+        }
+    }
+}
+
+template <typename W, typename X, int V>
+__global__ void __launch_bounds__(kSimtThreads) few_experts_simt_kernel(const FewArgs p) {
+    __shared__ SimtShared s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int A = p.T * p.k;
+    pdl_wait();  // the logits and the zeroed counters
+    int next = 0;
+    if (tid == 0) next = atomicAdd(&p.ctr->claim, 1);
+    few_plan(p, s.plan, kSimtTokens, kSimtThreads);
+    const int tiles_h = (p.F + kSimtRows - 1) / kSimtRows, tiles_o = (p.d + kSimtRows - 1) / kSimtRows;
+    const int groups = s.plan.groups, items_h = groups * tiles_h, items = items_h + groups * tiles_o;
+    for (;;) {
+        if (tid == 0) {
+            s.item = next;
+            s.go = 1;
+            if (next < items) {
+                const int mine = next;
+                next = atomicAdd(&p.ctr->claim, 1);  // the following item's claim runs while this one is computed
+                if (mine >= items_h)
+                    s.go = wait_counter_geq(&p.ctr->done[(mine - items_h) % groups], tiles_h, p.status, 71);
+            }
+        }
+        __syncthreads();
+        const int item = s.item;
+        if (item >= items || !s.go) break;
+        const bool second = item >= items_h;
+        const int g = second ? (item - items_h) % groups : item / tiles_h;
+        const int tile = second ? (item - items_h) / groups : item % tiles_h;
+        const int e = s.plan.g_expert[g], a0 = s.plan.g_first[g], m = s.plan.g_size[g];
+        const int row0 = tile * kSimtRows, rows = second ? p.d : p.F, K = second ? p.F : p.d;
+        const W *w = static_cast<const W *>(second ? p.w_out : p.w_in) + ((int64_t)e * rows + row0) * K;
+        if (second) {
+            const float *in[kSimtTokens];
+#pragma unroll
+            for (int j = 0; j < kSimtTokens; ++j) in[j] = p.h + (int64_t)(a0 + min(j, m - 1)) * p.F;
+            simt_dots<W, float, V>(w, rows - row0, K, in, m, warp, lane, s.red[warp]);
+        } else {
+            const X *in[kSimtTokens];
+#pragma unroll
+            for (int j = 0; j < kSimtTokens; ++j)
+                in[j] = static_cast<const X *>(p.x) + (int64_t)s.plan.token[a0 + min(j, m - 1)] * p.d;
+            simt_dots<W, X, V>(w, rows - row0, K, in, m, warp, lane, s.red[warp]);
+        }
+        __syncthreads();
+        if (tid < kSimtRows * kSimtTokens) {
+            const int j = tid / kSimtRows, r = tid % kSimtRows, row = row0 + r;
+            if (j < m && row < rows) {
+                float v = 0.f;
+#pragma unroll
+                for (int q = 0; q < kSimtWarps; ++q) v += s.red[q][r * kSimtTokens + j];
+                if (second) {
+                    if (p.w_out_scale != nullptr) v *= p.w_out_scale[(int64_t)e * p.d + row];
+                    p.o[(int64_t)(a0 + j) * p.d + row] = v;
+                } else {
+                    if (p.w_in_scale != nullptr) v *= p.w_in_scale[(int64_t)e * p.F + row];
+                    if (p.x_scale != nullptr) v *= p.x_scale[s.plan.token[a0 + j]];
+                    p.h[(int64_t)(a0 + j) * p.F + row] = v < 0.f ? 0.f : v;  // NaN stays NaN
+                }
+            }
+        }
+        __syncthreads();
+        if (tid == 0) {
+            __threadfence();
+            if (second) s.last = atomicAdd(&p.ctr->tile[tile], 1) == groups - 1;
+            else red_release_add_gpu(&p.ctr->done[g], 1);
+            __threadfence();
+        }
+        if (second) {
+            __syncthreads();
+            if (s.last) few_combine(p, s.plan, 1, A, row0, min(kSimtRows, p.d - row0), tid, kSimtThreads);
+        }
+        __syncthreads();
+    }
+}
+
+template <typename W, typename X, int V>
+cudaError_t experts_simt(const FewArgs &p, cudaStream_t stream) {
+    int per_sm = 0;
+    cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, few_experts_simt_kernel<W, X, V>,
+                                                                    kSimtThreads, 0);
+    if (err != cudaSuccess) return err;
+    return launch_kernel(few_experts_simt_kernel<W, X, V>, dim3(device_sm_count() * (per_sm < 1 ? 1 : per_sm)),
+                         dim3(kSimtThreads), 0, stream, true, p);
+}
+
+}  // namespace
+
+namespace {
+
+// Parts that the second dimension of a product may be cut into: enough to
+// give every SM work when few pairs keep few tiles, and 256 rows of partial
+// sums at most.
+int few_max_splits(int64_t pairs) {
+    const int64_t s = pairs > 0 ? 256 / pairs : 16;
+    return (int)(s < 2 ? 2 : s > 16 ? 16 : s);
+}
+
+struct FewSections {
+    size_t status, ctr, hmax, xmax, logits, h, o, total;
+};
+FewSections few_layout(const switch_dims_t &d, int top_k) {
+    const size_t A = (size_t)d.T * top_k, S = (size_t)few_max_splits((int64_t)A);
+    FewSections s{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    s.status = take(sizeof(DeviceStatus));
+    s.ctr = off;  // the counters and hmax right behind them are zeroed as one range
+    off += sizeof(FewCounters);
+    s.hmax = off;
+    take(S * A * 4);
+    s.xmax = take((size_t)d.T * 4);
+    s.logits = take((size_t)d.T * d.num_experts * 4);
+    s.h = take(S * A * (size_t)d.d_ff * 4);
+    s.o = take(S * A * (size_t)d.d_model * 4);
+    s.total = off;
+    return s;
+}
+
+}  // namespace
+
+size_t few_workspace_bytes(const switch_dims_t &dims, int top_k) { return few_layout(dims, top_k).total; }
+
+cudaError_t launch_layer_few(const switch_dims_t &dims, int x_dtype, FewArgs &p, void *workspace,
+                             cudaStream_t stream) {
+    const FewSections s = few_layout(dims, p.k);
+    uint8_t *b = static_cast<uint8_t *>(workspace);
+    p.status = reinterpret_cast<DeviceStatus *>(b + s.status);
+    p.ctr = reinterpret_cast<FewCounters *>(b + s.ctr);
+    p.hmax = reinterpret_cast<uint32_t *>(b + s.hmax);
+    p.xmax = reinterpret_cast<uint32_t *>(b + s.xmax);
+    p.logits = reinterpret_cast<float *>(b + s.logits);
+    p.h = reinterpret_cast<float *>(b + s.h);
+    p.o = reinterpret_cast<float *>(b + s.o);
+    if (p.T == 0) {
+        cudaError_t err = cudaMemsetAsync(p.status, 0, sizeof(DeviceStatus), stream);
+        if (err == cudaSuccess) err = cudaMemsetAsync(p.counts, 0, (size_t)p.N * 4, stream);
+        return err == cudaSuccess ? cudaMemsetAsync(p.aux, 0, 4, stream) : err;
+    }
+    const int zero_ints = (int)(sizeof(FewCounters) / 4) + few_max_splits(p.T * p.k) * p.T * p.k;
+    const cudaError_t err = launch_few_router(p, x_dtype, zero_ints, false, stream);
+    if (err != cudaSuccess) return err;
+    return launch_few_experts_simt(p, dims.dtype, x_dtype, stream);
+}
+
+cudaError_t launch_few_router(const FewArgs &p, int x_dtype, int zero_ints, bool want_xmax, cudaStream_t stream) {
+    launch_begin(K_FEW_ROUTER, stream);
+    if (x_dtype == SWITCH_BF16) router_typed<__nv_bfloat16, 4>(p, zero_ints, want_xmax, stream);
+    else if (x_dtype == SWITCH_E4M3) router_typed<uint8_t, 4>(p, zero_ints, want_xmax, stream);
+    else if (p.d % 4 == 0) router_typed<float, 4>(p, zero_ints, want_xmax, stream);
+    else router_typed<float, 1>(p, zero_ints, want_xmax, stream);
+    const cudaError_t err = cudaGetLastError();
+    launch_end(stream);
+    return err;
+}
+
+cudaError_t launch_few_experts_simt(const FewArgs &p, int w_dtype, int x_dtype, cudaStream_t stream) {
+    launch_begin(K_FEW_EXPERTS_SIMT, stream);
+    cudaError_t err;
+    if (w_dtype == SWITCH_BF16) err = experts_simt<__nv_bfloat16, __nv_bfloat16, 8>(p, stream);
+    else if (w_dtype == SWITCH_E4M3 && x_dtype == SWITCH_E4M3) err = experts_simt<uint8_t, uint8_t, 8>(p, stream);
+    else if (w_dtype == SWITCH_E4M3) err = experts_simt<uint8_t, __nv_bfloat16, 8>(p, stream);
+    else if (p.d % 4 == 0 && p.F % 4 == 0) err = experts_simt<float, float, 4>(p, stream);
+    else err = experts_simt<float, float, 1>(p, stream);
+    launch_end(stream);
+    return err;
+}
+
+}  // namespace switchmoe

@@ -46,6 +46,13 @@ enum KernelId : int32_t {
     K_BWD_ROUTER_TC_DX = 30,
     K_BWD_ROUTER_TC_DW = 31,
     K_BWD_ZERO_TAILS = 32,
+    K_NORM_FWD = 33,
+    K_NORM_BWD = 34,
+    K_NORM_DWEIGHT = 35,
+    K_QUANTIZE_ROWS = 36,
+    K_FEW_ROUTER = 37,
+    K_FEW_EXPERTS_SIMT = 38,
+    K_FEW_EXPERTS_TC = 39,
 };
 
 struct Workspace {
@@ -162,6 +169,26 @@ cudaError_t launch_ffn_tc_bwd_dx(const switch_dims_t &dims, const void *grad_z, 
                                  cudaStream_t stream);
 cudaError_t launch_ffn_tc_bwd_dw(const switch_dims_t &dims, const void *a, const void *b, const int32_t *counts,
                                  int rows, int nout, float *out, DeviceStatus *st, cudaStream_t stream);
+
+// Residual + norm, its gradient, rows in 8 bits.
+constexpr int kNormBwdBlocks = 296;  // blocks of the gradient kernel at most (two per SM): rows of its partial sums
+size_t norm_workspace_bytes(const switch_norm_dims_t &n);
+cudaError_t launch_norm_fwd(const switch_norm_dims_t &n, const void *residual, const void *delta, const float *weight,
+                            void *sum, void *out, float *scale, float *rstd, cudaStream_t stream);
+cudaError_t launch_norm_bwd(const switch_norm_dims_t &n, const void *sum, const float *weight, const float *rstd,
+                            const float *dout, const float *dsum, float *dres, float *dweight, void *workspace,
+                            cudaStream_t stream);
+cudaError_t launch_quantize_rows(int64_t rows, int cols, int dtype, const void *x, void *q, float *scale,
+                                 cudaStream_t stream);
+
+// The layer for a few tokens.  `x_dtype` is x's type, `dims.dtype` the experts'.
+struct FewArgs;
+size_t few_workspace_bytes(const switch_dims_t &dims, int top_k);
+// Sets the workspace pointers of `args` and launches the call's kernels.
+cudaError_t launch_layer_few(const switch_dims_t &dims, int x_dtype, FewArgs &args, void *workspace,
+                             cudaStream_t stream);
+cudaError_t launch_few_router(const FewArgs &p, int x_dtype, int zero_ints, bool want_xmax, cudaStream_t stream);
+cudaError_t launch_few_experts_simt(const FewArgs &p, int w_dtype, int x_dtype, cudaStream_t stream);
 
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
