@@ -358,10 +358,14 @@ cudaError_t launch_layer_few(const switch_dims_t &dims, int x_dtype, FewArgs &p,
         if (err == cudaSuccess) err = cudaMemsetAsync(p.counts, 0, (size_t)p.N * 4, stream);
         return err == cudaSuccess ? cudaMemsetAsync(p.aux, 0, 4, stream) : err;
     }
-    const int zero_ints = (int)(sizeof(FewCounters) / 4) + few_max_splits(p.T * p.k) * p.T * p.k;
-    const cudaError_t err = launch_few_router(p, x_dtype, zero_ints, false, stream);
+    const int splits = few_max_splits(p.T * p.k);
+    const bool tensor_cores = dims.dtype != SWITCH_F32 && !(dims.flags & SWITCH_FLAG_SIMT_FFN);
+    const bool cut_x = tensor_cores && dims.dtype == SWITCH_E4M3 && x_dtype == SWITCH_BF16;
+    const int zero_ints = (int)(sizeof(FewCounters) / 4) + (tensor_cores ? splits * p.T * p.k : 0);
+    const cudaError_t err = launch_few_router(p, x_dtype, zero_ints, cut_x, stream);
     if (err != cudaSuccess) return err;
-    return launch_few_experts_simt(p, dims.dtype, x_dtype, stream);
+    return tensor_cores ? launch_few_experts_tc(p, dims.dtype, x_dtype, splits, stream)
+                        : launch_few_experts_simt(p, dims.dtype, x_dtype, stream);
 }
 
 cudaError_t launch_few_router(const FewArgs &p, int x_dtype, int zero_ints, bool want_xmax, cudaStream_t stream) {

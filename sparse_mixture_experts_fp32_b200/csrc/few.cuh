@@ -52,7 +52,7 @@ struct FewPlan {
     float top[kFewMaxT], total[kFewMaxT];  // softmax maximum and sum of each token
     int cnt[kFewMaxN], base[kFewMaxN];
     int g_expert[kFewMaxA], g_first[kFewMaxA], g_size[kFewMaxA];
-    int groups;
+    int groups, largest;     // groups; positions of the largest one
 };
 
 // Every thread of a block of `threads` (a multiple of 32, at least 128) calls
@@ -120,7 +120,7 @@ __device__ inline void few_plan(const FewArgs &p, FewPlan &s, int group_max, int
     }
     __syncthreads();
     if (warp == 0) {
-        int pairs = 0, groups = 0;
+        int pairs = 0, groups = 0, largest = 0;
         for (int n0 = 0; n0 < p.N; n0 += 32) {
             const int n = n0 + lane;
             const int kept = n < p.N ? min(s.cnt[n], p.C) : 0;
@@ -138,10 +138,12 @@ __device__ inline void few_plan(const FewArgs &p, FewPlan &s, int group_max, int
                 s.g_first[at] = pairs + a - kept + j * group_max;
                 s.g_size[at] = min(group_max, kept - j * group_max);
             }
+            largest = max(largest, min(group_max, kept));
             pairs += __shfl_sync(0xffffffffu, a, 31);
             groups += __shfl_sync(0xffffffffu, g, 31);
         }
-        if (lane == 0) s.groups = groups;
+        largest = __reduce_max_sync(0xffffffffu, largest);
+        if (lane == 0) s.groups = groups, s.largest = largest;
     }
     __syncthreads();
     for (int i = tid; i < A; i += threads) {

@@ -1,0 +1,663 @@
+// The layer for a few tokens on tensor cores: bfloat16 and 8-bit experts
+// (few.cu describes the call and how blocks share the work).
+//
+// Both products are D[128 weight rows][columns] = W_tile . B^T: the weights are
+// the MMA's 128-row operand, streamed once from memory by TMA, and the columns
+// are the tokens of one expert (up to 32), so that an SM's tensor work per
+// 16 KB of weights is four MMAs whose cost is reading those 16 KB from shared
+// memory: 128 of the about 700 cycles that memory takes to deliver them.  That
+// leaves room to spend columns on precision:
+//  - bfloat16 experts: a column per token for x; the float32 hidden value h is
+//    cut into three bfloat16 terms (exact), a column each;
+//  - 8-bit experts run as kind::f8f6f4, both operands e4m3: x in bfloat16 is cut
+//    into two e4m3 terms, h into five: each term rounds what the ones before it
+//    left, scaled by 16 more, so n terms hold 4 n bits.  A power of two per token
+//    brings its largest value into [128, 256).  The epilogue adds the columns of
+//    a token with their scales.  (x given in 8 bits is one column as it is.)
+// The tensor core truncates each addition to its float32 accumulator: over a
+// long row of weights that biases sums by up to 1e-5 (measured: K = 4096, 256
+// MMAs in a chain: 4e-6; 16 in a chain: 2.4e-7).  So an accumulator takes four
+// ring stages (16 MMAs), and the epilogue warps add accumulators in float32
+// registers, rounding to nearest, while the next ones fill.
+//
+//   warp 0        claims items, loads weight tiles (TMA, 128-byte swizzle) into
+//                 a ring of 16 KB stages
+//   warp 1        issues the MMAs
+//   warps 2-5     epilogue: 32 weight rows each
+//   warps 6-13    build the column operand of every eighth stage: gather x rows,
+//                 or add the partial sums of h, apply ReLU and cut into terms
+// The ring runs on across items and from the first product into the second:
+// weights of the second product are on their way while the first is finished.
+// An item is a tile of 128 weight rows of one expert, cut along its length into
+// equal parts when there are few tiles (few_splits).
+#include <cuda.h>
+
+#include "few.cuh"
+
+namespace switchmoe {
+namespace {
+
+constexpr int kGroup = 32;        // tokens of a group
+constexpr int kStageA = 128 * 128;  // bytes: 128 weight rows x 128 bytes
+constexpr int kMaxStages = 12;
+constexpr int kRing = 215 * 1024;  // of the 227 KB a block may have: the plan and the barriers take 8 KB
+constexpr int kMaxBufs = 8;
+constexpr int kChain = 4;         // stages per accumulator
+constexpr int kBuilders = 8;
+constexpr int kTcThreads = 32 * (6 + kBuilders);
+constexpr int kQueue = 4;
+constexpr int kConsumers = 1 + 4 + kBuilders;  // warps that read the item queue
+
+template <bool E4M3, bool X8>
+struct Terms {
+    static constexpr int first = E4M3 ? (X8 ? 1 : 2) : 1;
+    static constexpr int second = E4M3 ? 5 : 3;
+};
+
+struct TcShared {
+    FewPlan plan;
+    uint64_t full_a[kMaxStages], full_b[kMaxStages], empty[kMaxStages];
+    uint64_t acc_full[kMaxBufs], acc_empty[kMaxBufs];
+    uint64_t q_full[kQueue], q_empty[kQueue];
+    uint64_t drain;
+    uint32_t tmem;
+    int queue[kQueue];
+    int splits_h, splits_o;
+};
+
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor for kind::f8f6f4 with e4m3 A and B and an fp32 accumulator.
+__device__ __forceinline__ uint32_t idesc_e4m3_f32(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
+// Parts that the length of a product is cut into: the least of (waves of
+// items) x (stages of an item + 2 for its epilogue and hand-over).
+__device__ __forceinline__ int few_splits(int tiles, int stages, int max_splits, int blocks) {
+    int best = 1, cost = ((tiles + blocks - 1) / blocks) * (stages + 2);
+    for (int s = 2; s <= max_splits && s <= stages; s *= 2) {
+        const int c = ((tiles * s + blocks - 1) / blocks) * ((stages + s - 1) / s + 2);
+        if (c < cost) best = s, cost = c;
+    }
+    return best;
+}
+
+// Work of the call, the same in every block.
+struct Work {
+    int groups, tiles_h, tiles_o, len_h, len_o, splits_h, splits_o, items_h, items;
+};
+struct Item {
+    bool second;
+    int g, tile, split, k0, k1;  // ring stages [k0, k1) of the row
+};
+__device__ __forceinline__ Item locate(const Work &w, int item) {
+    Item it;
+    it.second = item >= w.items_h;
+    if (!it.second) {
+        it.split = item % w.splits_h;
+        const int q = item / w.splits_h;
+        it.tile = q % w.tiles_h;
+        it.g = q / w.tiles_h;
+        it.k0 = it.split * w.len_h / w.splits_h;
+        it.k1 = (it.split + 1) * w.len_h / w.splits_h;
+    } else {  // all groups' parts of a tile of output rows follow one another
+        const int r = item - w.items_h;
+        it.g = r % w.groups;
+        const int q = r / w.groups;
+        it.split = q % w.splits_o;
+        it.tile = q / w.splits_o;
+        it.k0 = it.split * w.len_o / w.splits_o;
+        it.k1 = (it.split + 1) * w.len_o / w.splits_o;
+    }
+    return it;
+}
+
+// Next item from the queue, for one warp; -1: no more, or a wait gave up.
+__device__ __forceinline__ int next_item(TcShared &s, uint32_t &n, int lane, DeviceStatus *status) {
+    const int q = n % kQueue;
+    const uint32_t parity = (n / kQueue) & 1u;
+    ++n;
+    if (!mbar_wait(&s.q_full[q], parity, status, 81)) return -1;
+    const int item = s.queue[q];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.q_empty[q]);
+    return item;
+}
+
+// Power of two that brings a value with these bits into [128, 256) (0 stays,
+// tiny ones as far as 2^100), as its exponent; 1000: not finite.
+__device__ __forceinline__ int scale_exponent(uint32_t bits) {
+    const int e = (int)(bits >> 23) - 127;
+    if (bits == 0) return 0;
+    return e == 128 ? 1000 : min(100, 7 - e);
+}
+__device__ __forceinline__ float pow2(int k) { return __int_as_float((127 + min(127, k)) << 23); }  // k >= -126
+__device__ __forceinline__ float unscale(int k) { return k == 1000 ? __int_as_float(0x7fc00000) : pow2(-k); }
+
+// 16 values -> TERMS rows of 16 e4m3 bytes: term i holds what the terms before
+// it left, times 16^i.
+template <int TERMS>
+__device__ __forceinline__ void store_e4m3_terms(uint8_t *tile, int row0, int chunk, float (&v)[16]) {
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __nv_fp8x2_storage_t q =
+                __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+            if (i & 1) w[i >> 1] |= (uint32_t)q << 16;
+            else w[i >> 1] = q;
+            if (t + 1 < TERMS) {
+                const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(q, __NV_E4M3)));
+                v[2 * i] = (v[2 * i] - f.x) * 16.f;
+                v[2 * i + 1] = (v[2 * i + 1] - f.y) * 16.f;
+            }
+        }
+        const int row = row0 + t;
+        *reinterpret_cast<uint4 *>(tile + row * 128 + ((chunk ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+__device__ __forceinline__ void add4(float *v, const float *p) {
+    const float4 a = __ldcg(reinterpret_cast<const float4 *>(p));
+    v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+}
+
+// The column operand of stage `kc` of a first product: x rows.
+template <bool E4M3, bool X8>
+__device__ __forceinline__ void build_x(const FewArgs &p, const FewPlan &s, uint8_t *tile, int a0, int m, int kc,
+                                        int my_exp, int lane) {
+    const int tasks = m * 8;
+    if constexpr (!E4M3 || X8) {  // 16 bytes per task as they are
+        const uint8_t *x = static_cast<const uint8_t *>(p.x);
+        const int64_t row_bytes = (int64_t)p.d * (E4M3 ? 1 : 2);
+        for (int i0 = lane; i0 < tasks; i0 += 128) {
+            uint4 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + 32 * u, tok = i >> 3;
+                const int64_t at = (int64_t)kc * 128 + (i & 7) * 16;
+                v[u] = make_uint4(0, 0, 0, 0);
+                if (i < tasks && at < row_bytes)
+                    v[u] = __ldg(reinterpret_cast<const uint4 *>(x + (int64_t)s.token[a0 + tok] * row_bytes + at));
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + 32 * u, row = i >> 3;
+                if (i < tasks) *reinterpret_cast<uint4 *>(tile + row * 128 + (((i & 7) ^ (row & 7)) << 4)) = v[u];
+            }
+        }
+    } else {
+        const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(p.x);
+        for (int i0 = 0; i0 < tasks; i0 += 32) {  // whole warps: the exponents are exchanged
+            const int i = i0 + lane, tok = i >> 3, at = kc * 128 + (i & 7) * 16;
+            const float up = pow2(__shfl_sync(0xffffffffu, my_exp, tok & 31));
+            if (i >= tasks) continue;
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = 0.f;
+            if (at < p.d) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(x + (int64_t)s.token[a0 + tok] * p.d + at);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 a = __ldg(src + h);
+                    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[8 * h + 2 * j] = __uint_as_float(w[j] << 16) * up;
+                        v[8 * h + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * up;
+                    }
+                }
+            }
+            store_e4m3_terms<2>(tile, tok * 2, i & 7, v);
+        }
+    }
+}
+
+// The column operand of stage `kc` of a second product: ReLU of the summed
+// parts of h, in terms.
+template <bool E4M3>
+__device__ __forceinline__ void build_h(const FewArgs &p, uint8_t *tile, int A, int splits, int a0, int m, int kc,
+                                        int my_exp, int lane) {
+    constexpr int V = E4M3 ? 16 : 8;  // values per 16-byte chunk
+    const int tasks = m * 8;
+    for (int i0 = 0; i0 < tasks; i0 += 32) {
+        const int i = i0 + lane, tok = i >> 3, at = (kc * 8 + (i & 7)) * V;
+        const float up = E4M3 ? pow2(__shfl_sync(0xffffffffu, my_exp, tok & 31)) : 1.f;
+        if (i >= tasks) continue;
+        float v[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = 0.f;
+        if (at < p.F) {
+            const float *src = p.h + (int64_t)(a0 + tok) * p.F + at;
+            const int64_t step = (int64_t)A * p.F;
+#pragma unroll 2
+            for (int q = 0; q < splits; ++q) {
+#pragma unroll
+                for (int j = 0; j < V / 4; ++j) add4(v + 4 * j, src + q * step + 4 * j);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = v[j] < 0.f ? 0.f : v[j] * up;  // NaN stays NaN
+        if constexpr (E4M3) {
+            store_e4m3_terms<5>(tile, tok * 5, i & 7, v);
+        } else {
+            uint16_t t[3][8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                uint16_t c[3];
+                split_bf16x3(v[j], c);
+                t[0][j] = c[0], t[1][j] = c[1], t[2][j] = c[2];
+            }
+#pragma unroll
+            for (int c = 0; c < 3; ++c) {
+                const int row = tok * 3 + c;
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = (uint32_t)t[c][2 * j] | ((uint32_t)t[c][2 * j + 1] << 16);
+                *reinterpret_cast<uint4 *>(tile + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+}
+
+// v[j] += the accumulator's value for token j (its terms joined), m tokens.
+template <bool E4M3, int TERMS>
+__device__ __forceinline__ void add_accumulator(uint32_t taddr, int m, float (&v)[kGroup]) {
+#pragma unroll
+    for (int b = 0; b < kGroup / 8; ++b) {
+        if (b * 8 >= m) break;
+        uint32_t r[TERMS][8];
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) tmem_ld_32x32b_x8(taddr + (uint32_t)((b * TERMS + t) * 8), r[t]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float a = 0.f;  // from the smallest term up
+#pragma unroll
+            for (int t = TERMS - 1; t >= 0; --t) {
+                const int col = j * TERMS + t;
+                a = a * (E4M3 ? 0.0625f : 1.f) + __uint_as_float(r[col / 8][col % 8]);
+            }
+            v[b * 8 + j] += a;
+        }
+    }
+}
+
+// y of one output row for every token.
+__device__ __forceinline__ void combine_row(const FewArgs &p, const FewPlan &s, int splits, int A, int row) {
+    const int64_t step = (int64_t)A * p.d;
+    if (splits == 1) {
+#pragma unroll 4
+        for (int t = 0; t < p.T; ++t) {
+            float y = 0.f;
+            for (int c = 0; c < p.k; ++c) {
+                const int a = s.pos[t * p.k + c];
+                const float o = __ldcg(p.o + (int64_t)max(a, 0) * p.d + row);
+                if (a >= 0) y += s.gate[t * p.k + c] * o;
+            }
+            p.y[(int64_t)t * p.d + row] = y;
+        }
+    } else {
+        for (int t = 0; t < p.T; ++t) {
+            float y = 0.f;
+            for (int c = 0; c < p.k; ++c) {
+                const int a = s.pos[t * p.k + c];
+                if (a < 0) continue;
+                float o = 0.f;
+#pragma unroll 4
+                for (int q = 0; q < splits; ++q) o += __ldcg(p.o + q * step + (int64_t)a * p.d + row);
+                y += s.gate[t * p.k + c] * o;
+            }
+            p.y[(int64_t)t * p.d + row] = y;
+        }
+    }
+}
+
+// max_splits: parts of h and o that the workspace holds.
+template <bool E4M3, bool X8>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    few_experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_in, const __grid_constant__ CUtensorMap tmap_out,
+                          const FewArgs p, int max_splits) {
+    extern __shared__ uint8_t raw[];
+    __shared__ TcShared s;
+    uint8_t *ring_a = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int A = p.T * p.k;
+    if (warp == 1) {
+        if (lane == 0) {
+            for (int i = 0; i < kMaxStages; ++i) {
+                mbar_init(&s.full_a[i], 1);
+                mbar_init(&s.full_b[i], 1);
+                mbar_init(&s.empty[i], 1);
+            }
+            for (int i = 0; i < kMaxBufs; ++i) {
+                mbar_init(&s.acc_full[i], 1);
+                mbar_init(&s.acc_empty[i], 4);
+            }
+            for (int i = 0; i < kQueue; ++i) {
+                mbar_init(&s.q_full[i], 1);
+                mbar_init(&s.q_empty[i], kConsumers);
+            }
+            mbar_init(&s.drain, 1);
+            fence_barrier_init();
+        }
+        __syncwarp();
+        tmem_alloc(&s.tmem, 512);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        prefetch_tmap(&tmap_in);
+        prefetch_tmap(&tmap_out);
+    }
+    pdl_wait();  // the logits and the zeroed counters
+    int claimed = 0;
+    if (tid == 0) claimed = atomicAdd(&p.ctr->claim, 1);
+    few_plan(p, s.plan, kGroup, kTcThreads);
+    Work w;
+    w.groups = s.plan.groups;
+    w.tiles_h = (p.F + 127) / 128;
+    w.tiles_o = (p.d + 127) / 128;
+    w.len_h = (p.d * (E4M3 ? 1 : 2) + 127) / 128;
+    w.len_o = (p.F * (E4M3 ? 1 : 2) + 127) / 128;
+    w.splits_h = few_splits(w.groups * w.tiles_h, w.len_h, max_splits, gridDim.x);
+    w.splits_o = few_splits(w.groups * w.tiles_o, w.len_o, max_splits, gridDim.x);
+    w.items_h = w.groups * w.tiles_h * w.splits_h;
+    w.items = w.items_h + w.groups * w.tiles_o * w.splits_o;
+    // The ring and the accumulators are laid out for the call's largest group:
+    // bytes of a stage's column operand (whole 8-row swizzle atoms), stages, columns and number of accumulators.
+    constexpr int kTerms = Terms<E4M3, X8>::second;  // the larger of the two products'
+    const int b_bytes = (s.plan.largest * kTerms + 15) / 16 * 16 * 128;
+    const int stages = min(kMaxStages, kRing / (kStageA + b_bytes));
+    const int acc_cols = ((s.plan.largest + 7) / 8 * 8 * kTerms + 31) / 32 * 32;
+    const int bufs = min(512 / acc_cols, kMaxBufs);
+    uint8_t *ring_b = ring_a + stages * kStageA;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, parity_of = 0;
+            bool ok = true;
+            for (uint32_t n = 0; ok; ++n) {
+                const int q = n % kQueue, item = claimed;
+                if (!mbar_wait(&s.q_empty[q], ((n / kQueue) & 1u) ^ 1u, p.status, 82)) break;
+                s.queue[q] = item < w.items ? item : -1;
+                mbar_arrive(&s.q_full[q]);
+                if (item >= w.items) break;
+                claimed = atomicAdd(&p.ctr->claim, 1);  // the next item's claim runs while this one's loads are issued
+                const Item it = locate(w, item);
+                const int e = s.plan.g_expert[it.g];
+                for (int kc = it.k0; kc < it.k1; ++kc) {
+                    if (!mbar_wait(&s.empty[stage], phase ^ 1u, p.status, 83)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&s.full_a[stage], kStageA);
+                    tma_load_3d(ring_a + stage * kStageA, it.second ? &tmap_out : &tmap_in, &s.full_a[stage],
+                                kc * (E4M3 ? 128 : 64), it.tile * 128, e);
+                    issued |= 1u << stage;
+                    parity_of = (parity_of & ~(1u << stage)) | (phase << stage);
+                    if (++stage == stages) stage = 0, phase ^= 1u;
+                }
+            }
+            // every load has landed before the block may end
+            for (int i = 0; i < stages; ++i)
+                if (issued & (1u << i)) mbar_wait(&s.full_a[i], (parity_of >> i) & 1u, p.status, 84);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, acc_phase = 0, n = 0;
+            bool ok = true;
+            while (ok) {
+                const int q = n % kQueue;
+                if (!mbar_wait(&s.q_full[q], (n / kQueue) & 1u, p.status, 85)) break;
+                const int item = s.queue[q];
+                mbar_arrive(&s.q_empty[q]);
+                ++n;
+                if (item < 0) break;
+                const Item it = locate(w, item);
+                const int cols = s.plan.g_size[it.g] * (it.second ? Terms<E4M3, X8>::second : Terms<E4M3, X8>::first);
+                const int N = (cols + 15) / 16 * 16;
+                const uint32_t idesc = E4M3 ? idesc_e4m3_f32(128, N) : idesc_bf16_f32(128, N);
+                for (int kc = it.k0; ok && kc < it.k1;) {
+                    if (!mbar_wait(&s.acc_empty[buf], acc_phase ^ 1u, p.status, 86)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem + (uint32_t)(buf * acc_cols);
+                    const int end = min(kc + kChain, it.k1);
+                    for (uint32_t more = 0; kc < end; ++kc) {
+                        if (!mbar_wait(&s.full_a[stage], phase, p.status, 87) ||
+                            !mbar_wait(&s.full_b[stage], phase, p.status, 88)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t a_desc = smem_desc_sw128(ring_a + stage * kStageA);
+                        const uint64_t b_desc = smem_desc_sw128(ring_b + stage * b_bytes);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k, more = 1) {  // 32 bytes of every row each
+                            if constexpr (E4M3) tc_mma_f8(d, a_desc + 2 * k, b_desc + 2 * k, idesc, more);
+                            else tc_mma_bf16(d, a_desc + 2 * k, b_desc + 2 * k, idesc, more);
+                        }
+                        tc_commit(&s.empty[stage]);
+                        if (++stage == stages) stage = 0, phase ^= 1u;
+                    }
+                    if (!ok) break;
+                    tc_commit(&s.acc_full[buf]);
+                    if (++buf == bufs) buf = 0, acc_phase ^= 1u;
+                }
+            }
+            tc_commit(&s.drain);
+            mbar_wait(&s.drain, 0, p.status, 89);
+        }
+    } else if (warp < 6) {
+        const int quarter = warp & 3;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        int buf = 0;
+        uint32_t acc_phase = 0, n = 0;
+        bool ok = true;
+        while (ok) {
+            const int item = next_item(s, n, lane, p.status);
+            if (item < 0) break;
+            const Item it = locate(w, item);
+            const int e = s.plan.g_expert[it.g], a0 = s.plan.g_first[it.g], m = s.plan.g_size[it.g];
+            const int row = it.tile * 128 + quarter * 32 + lane, rows = it.second ? p.d : p.F;
+            const bool live = row < rows;
+            float v[kGroup];
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) v[j] = 0.f;
+            float scale = 1.f, own = 1.f;  // of the weight row; of token `lane` of the group
+            if constexpr (E4M3) {
+                if (live) scale = __ldg((it.second ? p.w_out_scale : p.w_in_scale) + (int64_t)e * rows + row);
+                if (!it.second && lane < m) {
+                    const int t = s.plan.token[a0 + lane];
+                    own = X8 ? __ldg(p.x_scale + t) : unscale(scale_exponent(__ldcg(p.xmax + t)));
+                }
+            }
+            for (int kc = it.k0; kc < it.k1; kc += kChain) {
+                if (!mbar_wait(&s.acc_full[buf], acc_phase, p.status, 90)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t at = lanes + (uint32_t)(buf * acc_cols);
+                if (it.second) add_accumulator<E4M3, Terms<E4M3, X8>::second>(at, m, v);
+                else add_accumulator<E4M3, Terms<E4M3, X8>::first>(at, m, v);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.acc_empty[buf]);
+                if (++buf == bufs) buf = 0, acc_phase ^= 1u;
+            }
+            if (!ok) break;
+            if constexpr (E4M3) {
+                // an accumulator of the second product exists once every part of h does: so do their maxima
+                if (it.second && lane < m) {
+                    float top = 0.f;
+                    for (int q = 0; q < w.splits_h; ++q) top += __uint_as_float(__ldcg(p.hmax + q * A + a0 + lane));
+                    own = unscale(scale_exponent(__float_as_uint(top)));
+                }
+            }
+            float *out = it.second ? p.o + ((int64_t)it.split * A + a0) * p.d : p.h + ((int64_t)it.split * A + a0) * p.F;
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) {
+                if (j >= m) break;
+                float u = v[j];
+                if constexpr (E4M3) {
+                    u = u * __shfl_sync(0xffffffffu, own, j) * scale;
+                    if (!it.second) {
+                        const uint32_t top = __reduce_max_sync(0xffffffffu, live ? __float_as_uint(u) & 0x7fffffffu : 0u);
+                        if (lane == 0) atomicMax(p.hmax + it.split * A + a0 + j, top);
+                    }
+                }
+                if (live) out[(int64_t)j * rows + row] = u;
+            }
+            __syncwarp();
+            int last = 0;
+            if (lane == 0) {
+                __threadfence();
+                if (it.second)
+                    last = atomicAdd(&p.ctr->tile[it.tile * 4 + quarter], 1) == w.groups * w.splits_o - 1;
+                else red_release_add_gpu(&p.ctr->done[it.g], 1);
+                __threadfence();
+            }
+            if (__shfl_sync(0xffffffffu, last, 0) && live) combine_row(p, s.plan, w.splits_o, A, row);
+        }
+    } else {
+        // No more builders than stages: one that is a whole lap of the ring ahead of
+        // another would take the parity of an older phase for that of the one it waits for.
+        const int builders = min(kBuilders, stages), me = warp - 6;
+        int stage = 0;
+        uint32_t phase = 0, n = 0;
+        int count = 0;
+        bool ok = true;
+        while (ok) {
+            const int item = next_item(s, n, lane, p.status);
+            if (item < 0) break;
+            const Item it = locate(w, item);
+            const int a0 = s.plan.g_first[it.g], m = s.plan.g_size[it.g];
+            int my_exp = 0;  // 8-bit experts: exponent of token `lane`'s scale
+            bool ready = false;
+            for (int kc = it.k0; kc < it.k1; ++kc, ++count) {
+                if (count % builders == me) {
+                    if (!ready) {
+                        ready = true;
+                        if (it.second) {
+                            int fine = 1;
+                            if (lane == 0)
+                                fine = wait_counter_geq(&p.ctr->done[it.g], 4 * w.tiles_h * w.splits_h, p.status, 91);
+                            ok = __shfl_sync(0xffffffffu, fine, 0) != 0;
+                            if (!ok) break;
+                        }
+                        if constexpr (E4M3) {
+                            if (lane < m) {
+                                if (it.second) {
+                                    float top = 0.f;
+                                    for (int q = 0; q < w.splits_h; ++q)
+                                        top += __uint_as_float(__ldcg(p.hmax + q * A + a0 + lane));
+                                    my_exp = scale_exponent(__float_as_uint(top));
+                                } else if (!X8) {
+                                    my_exp = scale_exponent(__ldcg(p.xmax + s.plan.token[a0 + lane]));
+                                }
+                            }
+                        }
+                    }
+                    if (!mbar_wait(&s.empty[stage], phase ^ 1u, p.status, 92)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *tile = ring_b + stage * b_bytes;
+                    if (it.second) build_h<E4M3>(p, tile, A, w.splits_h, a0, m, kc, my_exp, lane);
+                    else build_x<E4M3, X8>(p, s.plan, tile, a0, m, kc, my_exp, lane);
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.full_b[stage]);
+                }
+                if (++stage == stages) stage = 0, phase ^= 1u;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeTiledFn>(f);
+    }();
+    return fn;
+}
+
+// [E][rows][K] weights, box = 128 rows x 128 bytes, 128-byte swizzle; zeros past an expert's rows and K.
+bool weight_map(CUtensorMap *map, const void *ptr, int E, int rows, int K, bool e4m3) {
+    const EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t size = e4m3 ? 1 : 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)rows, (cuuint64_t)E};
+    const cuuint64_t strides[2] = {(cuuint64_t)K * size, (cuuint64_t)rows * K * size};
+    const cuuint32_t box[3] = {e4m3 ? 128u : 64u, 128u, 1u}, unit[3] = {1, 1, 1};
+    return fn(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr),
+              dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool E4M3, bool X8>
+cudaError_t experts_tc(const FewArgs &p, int max_splits, cudaStream_t stream) {
+    CUtensorMap in, out;
+    if (!weight_map(&in, p.w_in, p.N, p.F, p.d, E4M3) || !weight_map(&out, p.w_out, p.N, p.d, p.F, E4M3))
+        return cudaErrorInvalidValue;
+    const cudaError_t err = cudaFuncSetAttribute(few_experts_tc_kernel<E4M3, X8>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kRing);
+    if (err != cudaSuccess) return err;
+    return launch_kernel(few_experts_tc_kernel<E4M3, X8>, dim3(device_sm_count()), dim3(kTcThreads), 1024 + kRing,
+                         stream, true, in, out, p, max_splits);
+}
+
+}  // namespace
+
+cudaError_t launch_few_experts_tc(const FewArgs &p, int w_dtype, int x_dtype, int max_splits, cudaStream_t stream) {
+    launch_begin(K_FEW_EXPERTS_TC, stream);
+    cudaError_t err;
+    if (w_dtype == SWITCH_BF16) err = experts_tc<false, false>(p, max_splits, stream);
+    else if (x_dtype == SWITCH_E4M3) err = experts_tc<true, true>(p, max_splits, stream);
+    else err = experts_tc<true, false>(p, max_splits, stream);
+    launch_end(stream);
+    return err;
+}
+
+}  // namespace switchmoe

@@ -188,6 +188,7 @@ size_t few_workspace_bytes(const switch_dims_t &dims, int top_k);
 cudaError_t launch_layer_few(const switch_dims_t &dims, int x_dtype, FewArgs &args, void *workspace,
                              cudaStream_t stream);
 cudaError_t launch_few_router(const FewArgs &p, int x_dtype, int zero_ints, bool want_xmax, cudaStream_t stream);
+cudaError_t launch_few_experts_tc(const FewArgs &p, int w_dtype, int x_dtype, int max_splits, cudaStream_t stream);
 cudaError_t launch_few_experts_simt(const FewArgs &p, int w_dtype, int x_dtype, cudaStream_t stream);
 
 // Number of SMs of the current device (cached per device).

@@ -135,7 +135,7 @@ WX = [("f32", None), ("bf16", None), ("e4m3", None), ("e4m3", "e4m3")]
 @pytest.mark.parametrize("w,x", WX)
 @pytest.mark.parametrize("T,d,F,N", [(1, 64, 64, 2), (1, 512, 1088, 5), (2, 64, 192, 3), (7, 192, 320, 4),
                                      (8, 1024, 256, 16), (9, 256, 1024, 64), (33, 320, 448, 3), (64, 128, 576, 2),
-                                     (64, 192, 64, 256), (31, 2112, 64, 8)])
+                                     (64, 192, 64, 256), (31, 2112, 64, 8), (32, 1024, 1024, 128)])
 def test_few(T, d, F, N, w, x, k):
     p = make(T, d, F, N, w, x, seed=T + d)
     check(run(p, k), plain(p, k, T), k)
