@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(kRouterThreads)
     __shared__ uint32_t big[kRouterThreads / 32][TT];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int e0 = blockIdx.x * TE, t0 = blockIdx.y * TT;
+    pdl_wait();  // x; and the call before this one may still use the workspace
     pdl_launch_dependents();
     {  // the second kernel's counters and maxima, and the status word
         const int blocks = gridDim.x * gridDim.y, me = blockIdx.y * gridDim.x + blockIdx.x;
@@ -95,6 +96,8 @@ __global__ void __launch_bounds__(kRouterThreads)
 #pragma unroll
         for (int e = 0; e < TE; ++e) acc[e][t] = 0.f;
     }
+    // several steps' loads in flight: rows of W_r come from memory, 1 us away
+#pragma unroll(TE * TT == 1 ? 8 : TE == 1 ? 4 : 2)
     for (int j = tid * V; j < p.d; j += kRouterThreads * V) {
         float wv[TE][V];
 #pragma unroll
@@ -146,17 +149,18 @@ __global__ void __launch_bounds__(kRouterThreads)
     }
 }
 
+template <typename X, int V, int TE, int TT>
+cudaError_t router_launch(const FewArgs &p, int zero_ints, int want_xmax, cudaStream_t stream) {
+    return launch_kernel(few_router_kernel<X, V, TE, TT>, dim3((p.N + TE - 1) / TE, (p.T + TT - 1) / TT),
+                         dim3(kRouterThreads), 0, stream, true, p, zero_ints, want_xmax);
+}
+
 template <typename X, int V>
-void router_typed(const FewArgs &p, int zero_ints, int want_xmax, cudaStream_t stream) {
+cudaError_t router_typed(const FewArgs &p, int zero_ints, int want_xmax, cudaStream_t stream) {
     // one expert per block for the most blocks in flight; with many blocks four, so that a row of x serves four
-    if (p.T == 1) {
-        few_router_kernel<X, V, 1, 1><<<dim3(p.N, 1), kRouterThreads, 0, stream>>>(p, zero_ints, want_xmax);
-    } else if (p.N * ((p.T + 7) / 8) <= 592) {
-        few_router_kernel<X, V, 1, 8><<<dim3(p.N, (p.T + 7) / 8), kRouterThreads, 0, stream>>>(p, zero_ints, want_xmax);
-    } else {
-        few_router_kernel<X, V, 4, 8>
-            <<<dim3((p.N + 3) / 4, (p.T + 7) / 8), kRouterThreads, 0, stream>>>(p, zero_ints, want_xmax);
-    }
+    if (p.T == 1) return router_launch<X, V, 1, 1>(p, zero_ints, want_xmax, stream);
+    if (p.N * ((p.T + 7) / 8) <= 592) return router_launch<X, V, 1, 8>(p, zero_ints, want_xmax, stream);
+    return router_launch<X, V, 4, 8>(p, zero_ints, want_xmax, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -220,11 +224,11 @@ template <typename W, typename X, int V>
 __global__ void __launch_bounds__(kSimtThreads) few_experts_simt_kernel(const FewArgs p) {
     __shared__ SimtShared s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int A = p.T * p.k;
     pdl_wait();  // the logits and the zeroed counters
     int next = 0;
     if (tid == 0) next = atomicAdd(&p.ctr->claim, 1);
     few_plan(p, s.plan, kSimtTokens, kSimtThreads);
+    if (tid < 128) few_gates(p, s.plan, tid, blockIdx.x == 0);
     const int tiles_h = (p.F + kSimtRows - 1) / kSimtRows, tiles_o = (p.d + kSimtRows - 1) / kSimtRows;
     const int groups = s.plan.groups, items_h = groups * tiles_h, items = items_h + groups * tiles_o;
     for (;;) {
@@ -278,17 +282,26 @@ __global__ void __launch_bounds__(kSimtThreads) few_experts_simt_kernel(const Fe
         }
         __syncthreads();
         if (tid == 0) {
-            __threadfence();
-            if (second) s.last = atomicAdd(&p.ctr->tile[tile], 1) == groups - 1;
+            if (second) s.last = atom_add_acq_rel_gpu(&p.ctr->tile[tile], 1) == groups - 1;
             else red_release_add_gpu(&p.ctr->done[g], 1);
-            __threadfence();
         }
         if (second) {
             __syncthreads();
-            if (s.last) few_combine(p, s.plan, 1, A, row0, min(kSimtRows, p.d - row0), tid, kSimtThreads);
+            if (s.last) {  // y of the tile's rows for every token
+                for (int i = tid; i < p.T * kSimtRows; i += kSimtThreads) {
+                    const int t = i / kSimtRows, row = row0 + i % kSimtRows;
+                    float y = 0.f;
+                    for (int c = 0; c < p.k; ++c) {
+                        const int a = s.plan.pos[t * p.k + c];
+                        if (a >= 0 && row < p.d) y += s.plan.gate[t * p.k + c] * __ldcg(p.o + (int64_t)a * p.d + row);
+                    }
+                    if (row < p.d) p.y[(int64_t)t * p.d + row] = y;
+                }
+            }
         }
         __syncthreads();
     }
+    pdl_launch_dependents();
 }
 
 template <typename W, typename X, int V>
@@ -305,16 +318,15 @@ cudaError_t experts_simt(const FewArgs &p, cudaStream_t stream) {
 
 namespace {
 
-// Parts that the second dimension of a product may be cut into: enough to
-// give every SM work when few pairs keep few tiles, and 256 rows of partial
-// sums at most.
+// Parts that the length of a product may be cut into: enough to give every SM
+// work when few pairs keep few tiles, and 512 rows of partial sums at most.
 int few_max_splits(int64_t pairs) {
-    const int64_t s = pairs > 0 ? 256 / pairs : 16;
-    return (int)(s < 2 ? 2 : s > 16 ? 16 : s);
+    const int64_t s = pairs > 0 ? 512 / pairs : 16;
+    return (int)(s > 16 ? 16 : s);
 }
 
 struct FewSections {
-    size_t status, ctr, hmax, xmax, logits, h, o, total;
+    size_t status, ctr, hmax, parts, xmax, logits, h, o, total;
 };
 FewSections few_layout(const switch_dims_t &d, int top_k) {
     const size_t A = (size_t)d.T * top_k, S = (size_t)few_max_splits((int64_t)A);
@@ -326,10 +338,13 @@ FewSections few_layout(const switch_dims_t &d, int top_k) {
         return at;
     };
     s.status = take(sizeof(DeviceStatus));
-    s.ctr = off;  // the counters and hmax right behind them are zeroed as one range
+    s.ctr = off;  // the counters, hmax and parts right behind one another are zeroed as one range
     off += sizeof(FewCounters);
     s.hmax = off;
-    take(S * A * 4);
+    off += S * A * 4;
+    s.parts = off;
+    take((size_t)((d.d_model + 127) / 128) * 4 * (size_t)d.T * 4);
+    off = (off + 255) / 256 * 256;
     s.xmax = take((size_t)d.T * 4);
     s.logits = take((size_t)d.T * d.num_experts * 4);
     s.h = take(S * A * (size_t)d.d_ff * 4);
@@ -349,6 +364,7 @@ cudaError_t launch_layer_few(const switch_dims_t &dims, int x_dtype, FewArgs &p,
     p.status = reinterpret_cast<DeviceStatus *>(b + s.status);
     p.ctr = reinterpret_cast<FewCounters *>(b + s.ctr);
     p.hmax = reinterpret_cast<uint32_t *>(b + s.hmax);
+    p.parts = reinterpret_cast<int32_t *>(b + s.parts);
     p.xmax = reinterpret_cast<uint32_t *>(b + s.xmax);
     p.logits = reinterpret_cast<float *>(b + s.logits);
     p.h = reinterpret_cast<float *>(b + s.h);
@@ -361,7 +377,8 @@ cudaError_t launch_layer_few(const switch_dims_t &dims, int x_dtype, FewArgs &p,
     const int splits = few_max_splits(p.T * p.k);
     const bool tensor_cores = dims.dtype != SWITCH_F32 && !(dims.flags & SWITCH_FLAG_SIMT_FFN);
     const bool cut_x = tensor_cores && dims.dtype == SWITCH_E4M3 && x_dtype == SWITCH_BF16;
-    const int zero_ints = (int)(sizeof(FewCounters) / 4) + (tensor_cores ? splits * p.T * p.k : 0);
+    const int zero_ints =
+        (int)(sizeof(FewCounters) / 4) + (tensor_cores ? splits * p.T * p.k + (p.d + 127) / 128 * 4 * p.T : 0);
     const cudaError_t err = launch_few_router(p, x_dtype, zero_ints, cut_x, stream);
     if (err != cudaSuccess) return err;
     return tensor_cores ? launch_few_experts_tc(p, dims.dtype, x_dtype, splits, stream)
@@ -370,11 +387,11 @@ cudaError_t launch_layer_few(const switch_dims_t &dims, int x_dtype, FewArgs &p,
 
 cudaError_t launch_few_router(const FewArgs &p, int x_dtype, int zero_ints, bool want_xmax, cudaStream_t stream) {
     launch_begin(K_FEW_ROUTER, stream);
-    if (x_dtype == SWITCH_BF16) router_typed<__nv_bfloat16, 4>(p, zero_ints, want_xmax, stream);
-    else if (x_dtype == SWITCH_E4M3) router_typed<uint8_t, 4>(p, zero_ints, want_xmax, stream);
-    else if (p.d % 4 == 0) router_typed<float, 4>(p, zero_ints, want_xmax, stream);
-    else router_typed<float, 1>(p, zero_ints, want_xmax, stream);
-    const cudaError_t err = cudaGetLastError();
+    cudaError_t err;
+    if (x_dtype == SWITCH_BF16) err = router_typed<__nv_bfloat16, 4>(p, zero_ints, want_xmax, stream);
+    else if (x_dtype == SWITCH_E4M3) err = router_typed<uint8_t, 4>(p, zero_ints, want_xmax, stream);
+    else if (p.d % 4 == 0) err = router_typed<float, 4>(p, zero_ints, want_xmax, stream);
+    else err = router_typed<float, 1>(p, zero_ints, want_xmax, stream);
     launch_end(stream);
     return err;
 }

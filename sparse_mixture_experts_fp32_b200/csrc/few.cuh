@@ -33,7 +33,8 @@ struct FewArgs {
     DeviceStatus *status;
     FewCounters *ctr;
     uint32_t *xmax;    // [T] bits of max |x| (8-bit experts with bfloat16 x)
-    uint32_t *hmax;    // [kFewMaxSplit][A] bits of max |partial sum| of a pair's hidden row
+    uint32_t *hmax;    // [splits][A] bits of max |partial sum| of a pair's hidden row (tensor cores)
+    int32_t *parts;    // [ceil(d / 128) * 4][T] finished parts of 32 values of a token's y (tensor cores)
     float *logits;     // [T][N]
     float *h;          // [splits][A][F] first product (before ReLU where it is split)
     float *o;          // [splits][A][d] second product
@@ -49,146 +50,181 @@ struct FewPlan {
     int pos[kFewMaxA];       // [t * k + c] -> position, -1: dropped
     int token[kFewMaxA];     // [position] -> token
     uint32_t order[kFewMaxA / 4];  // expert of every pair, a byte each, first choices before second ones
-    float top[kFewMaxT], total[kFewMaxT];  // softmax maximum and sum of each token
-    int cnt[kFewMaxN], base[kFewMaxN];
+    int cnt[kFewMaxN], first[kFewMaxN], base[kFewMaxN];  // pairs, first choices, first position of each expert
     int g_expert[kFewMaxA], g_first[kFewMaxA], g_size[kFewMaxA];
+    int part[kFewMaxN / 32];
+    double aux[4];
     int groups, largest;     // groups; positions of the largest one
 };
 
-// Every thread of a block of `threads` (a multiple of 32, at least 128) calls
-// this; block 0 also writes the call's routing outputs.  T and N are small
-// (64 x 256 logits at most), so that every block deciding for itself costs less
-// than another kernel or a grid-wide wait would.
+// Bits whose unsigned order is the order of floats; NaN is below everything.
+__device__ __forceinline__ uint32_t ordered_bits(float v) {
+    const uint32_t b = __float_as_uint(v + 0.f);  // -0 and 0 tie
+    return v != v ? 0u : b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+__device__ __forceinline__ void few_logits(const FewArgs &p, int t, int lane, float (&v)[kFewMaxN / 32]) {
+#pragma unroll
+    for (int i = 0; i < kFewMaxN / 32; ++i) {
+        const int n = 32 * i + lane;
+        v[i] = n < p.N ? __ldcg(p.logits + (int64_t)t * p.N + n) : -INFINITY;
+    }
+}
+
+// Lowest index of the largest logit but expert `skip`'s, for a warp.
+__device__ __forceinline__ int few_argmax(const uint32_t (&key)[kFewMaxN / 32], int N, int skip, int lane) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < kFewMaxN / 32; ++i) {
+        if (32 * i >= N) break;
+        if (32 * i + lane < N && 32 * i + lane != skip) best = max(best, key[i]);
+    }
+    best = __reduce_max_sync(0xffffffffu, best);
+    int at = -1;
+#pragma unroll
+    for (int i = 0; i < kFewMaxN / 32; ++i) {
+        if (32 * i >= N || at >= 0) break;
+        const int n = 32 * i + lane;
+        const uint32_t hit = __ballot_sync(0xffffffffu, n < N && n != skip && key[i] == best);
+        if (hit) at = 32 * i + __ffs(hit) - 1;
+    }
+    return at;
+}
+
+// Every thread of a block of `threads` (a multiple of 32, at least 256) calls
+// this.  T and N are small (64 x 256 logits at most), so that every block
+// deciding for itself costs less than another kernel or a grid-wide wait would.
+// It stands before the first weight that a block can ask for, so it does only
+// what the work list needs: the gates are few_gates', later.
 __device__ inline void few_plan(const FewArgs &p, FewPlan &s, int group_max, int threads) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = threads >> 5;
     const int A = p.T * p.k;
-    for (int n = tid; n < p.N; n += threads) s.cnt[n] = 0;
-    for (int i = tid; i < kFewMaxA / 4; i += threads) s.order[i] = 0;
-    __syncthreads();
+    for (int n = tid; n < p.N; n += threads) s.cnt[n] = s.first[n] = 0;
+    if (tid == 0) s.largest = 0;
+#pragma unroll 1
     for (int t = warp; t < p.T; t += warps) {
         float v[kFewMaxN / 32];
+        few_logits(p, t, lane, v);
+        uint32_t key[kFewMaxN / 32];
 #pragma unroll
-        for (int i = 0; i < kFewMaxN / 32; ++i) {
-            const int n = 32 * i + lane;
-            v[i] = n < p.N ? __ldcg(p.logits + (int64_t)t * p.N + n) : -INFINITY;
-        }
-        int first = -1;
-        float top = 0.f;
-        for (int c = 0; c < p.k; ++c) {
-            float best = -INFINITY;
-            int at = INT32_MAX;
-#pragma unroll
-            for (int i = 0; i < kFewMaxN / 32; ++i) {
-                const int n = 32 * i + lane;
-                if (n < p.N && n != first && (v[i] > best || (v[i] == best && n < at))) best = v[i], at = n;
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const float b = __shfl_xor_sync(0xffffffffu, best, o);
-                const int a = __shfl_xor_sync(0xffffffffu, at, o);
-                if (b > best || (b == best && a < at)) best = b, at = a;
-            }
-            if (at == INT32_MAX) at = first == 0 ? 1 : 0;  // no logit compares (NaN): any expert, with a NaN gate
-            if (c == 0) {
-                top = best;
-                float sum = 0.f;
-#pragma unroll
-                for (int i = 0; i < kFewMaxN / 32; ++i)
-                    if (32 * i + lane < p.N) sum += expf(v[i] - top);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (lane == 0) s.top[t] = top, s.total[t] = sum;
-                first = at;
-                __syncwarp();
-            }
-            if (lane == 0) {
-                s.expert[t * p.k + c] = at;
-                s.gate[t * p.k + c] = expf(best - top) / s.total[t];
-                reinterpret_cast<uint8_t *>(s.order)[c * p.T + t] = (uint8_t)at;
+        for (int i = 0; i < kFewMaxN / 32; ++i) key[i] = ordered_bits(v[i]);
+        const int first = few_argmax(key, p.N, -1, lane);
+        const int second = p.k == 2 ? few_argmax(key, p.N, first, lane) : 0;
+        if (lane == 0) {
+            s.expert[t * p.k] = first;
+            reinterpret_cast<uint8_t *>(s.order)[t] = (uint8_t)first;
+            if (p.k == 2) {
+                s.expert[2 * t + 1] = second;
+                reinterpret_cast<uint8_t *>(s.order)[p.T + t] = (uint8_t)second;
             }
         }
     }
     __syncthreads();
     for (int i = tid; i < A; i += threads) {  // rank among the pairs of its expert; first choices come first
-        const int t = i % p.T, c = i / p.T, e = s.expert[t * p.k + c];
+        const int c = i >= p.T, t = c ? i - p.T : i, e = s.expert[t * p.k + c];
         const uint32_t four = (uint32_t)e * 0x01010101u;
         int rank = 0;
+#pragma unroll 4
         for (int w = 0; w < i / 4; ++w) rank += __popc(__vcmpeq4(s.order[w], four)) >> 3;
         if (i & 3) rank += __popc(__vcmpeq4(s.order[i >> 2], four) & ((1u << (8 * (i & 3))) - 1u)) >> 3;
         s.slot[t * p.k + c] = rank < p.C ? rank : -1;
         atomicAdd(&s.cnt[e], 1);
+        if (c == 0) atomicAdd(&s.first[e], 1);
     }
     __syncthreads();
-    if (warp == 0) {
-        int pairs = 0, groups = 0, largest = 0;
-        for (int n0 = 0; n0 < p.N; n0 += 32) {
-            const int n = n0 + lane;
-            const int kept = n < p.N ? min(s.cnt[n], p.C) : 0;
-            const int mine = (kept + group_max - 1) / group_max;
-            int a = kept, g = mine;
+    int kept = 0, mine = 0, run = 0;
+    if (warp < kFewMaxN / 32) {  // positions (low half) and groups (high half) before each expert
+        kept = tid < p.N ? min(s.cnt[tid], p.C) : 0;
+        mine = (kept + group_max - 1) / group_max;
+        run = kept | mine << 16;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int ua = __shfl_up_sync(0xffffffffu, a, o), ug = __shfl_up_sync(0xffffffffu, g, o);
-                if (lane >= o) a += ua, g += ug;
-            }
-            if (n < p.N) s.base[n] = pairs + a - kept;
-            for (int j = 0; j < mine; ++j) {
-                const int at = groups + g - mine + j;
-                s.g_expert[at] = n;
-                s.g_first[at] = pairs + a - kept + j * group_max;
-                s.g_size[at] = min(group_max, kept - j * group_max);
-            }
-            largest = max(largest, min(group_max, kept));
-            pairs += __shfl_sync(0xffffffffu, a, 31);
-            groups += __shfl_sync(0xffffffffu, g, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += u;
         }
-        largest = __reduce_max_sync(0xffffffffu, largest);
-        if (lane == 0) s.groups = groups, s.largest = largest;
+        if (lane == 31) s.part[warp] = run;
+        const int largest = __reduce_max_sync(0xffffffffu, min(kept, group_max));
+        if (lane == 0) atomicMax(&s.largest, largest);
+    }
+    __syncthreads();
+    if (warp < kFewMaxN / 32) {
+        int all = 0;
+#pragma unroll
+        for (int q = 0; q < kFewMaxN / 32; ++q) {
+            if (q < warp) run += s.part[q];
+            all += s.part[q];
+        }
+        const int a = (run & 0xffff) - kept, g = (run >> 16) - mine;
+        if (tid < p.N) s.base[tid] = a;
+        for (int j = 0; j < mine; ++j) {
+            s.g_expert[g + j] = tid;
+            s.g_first[g + j] = a + j * group_max;
+            s.g_size[g + j] = min(group_max, kept - j * group_max);
+        }
+        if (tid == 0) s.groups = all >> 16;
     }
     __syncthreads();
     for (int i = tid; i < A; i += threads) {
         const int at = s.slot[i] < 0 ? -1 : s.base[s.expert[i]] + s.slot[i];
         s.pos[i] = at;
-        if (at >= 0) s.token[at] = i / p.k;
-    }
-    if (blockIdx.x == 0) {
-        for (int i = tid; i < A; i += threads) p.expert[i] = s.expert[i], p.gate[i] = s.gate[i], p.slot[i] = s.slot[i];
-        for (int n = tid; n < p.N; n += threads) p.counts[n] = s.cnt[n];
-        if (warp == 0) {  // aux = N sum_n (first choices of n / T) (mean_t p_n): float64, in a fixed order
-            double sum = 0.0;
-            for (int n = lane; n < p.N; n += 32) {
-                double prob = 0.0;
-                int f = 0;
-                for (int t = 0; t < p.T; ++t) {
-                    prob += (double)(expf(__ldcg(p.logits + (int64_t)t * p.N + n) - s.top[t]) / s.total[t]);
-                    f += s.expert[t * p.k] == n;
-                }
-                sum += (double)f * prob;
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == 0) *p.aux = (float)(sum * (double)p.N / ((double)p.T * (double)p.T));
-        }
+        if (at >= 0) s.token[at] = p.k == 2 ? i >> 1 : i;
     }
     __syncthreads();
 }
 
-// y of the output rows [row0, row0 + rows) for all tokens, by the block that
-// finished the rows' last item; `threads` threads call it (tid < threads).
-__device__ inline void few_combine(const FewArgs &p, const FewPlan &s, int splits, int A, int row0, int rows, int tid,
-                                   int threads) {
-    for (int i = tid; i < p.T * rows; i += threads) {
-        const int t = i / rows, row = row0 + i % rows;
-        float y = 0.f;
-        for (int c = 0; c < p.k; ++c) {
-            const int a = s.pos[t * p.k + c];
-            if (a < 0) continue;
-            float o = 0.f;
-            for (int q = 0; q < splits; ++q) o += __ldcg(p.o + ((int64_t)q * A + a) * p.d + row);
-            y += s.gate[t * p.k + c] * o;
+// The gates, by four warps (`tid` = 0..127) that share named barrier 1; with
+// `outputs` (one block) the call's routing outputs too.
+// aux = N / T^2 sum_t sum_n f_n p_tn, f_n the first choices of expert n:
+// float64, in a fixed order.
+__device__ inline void few_gates(const FewArgs &p, FewPlan &s, int tid, bool outputs) {
+    const int warp = tid >> 5, lane = tid & 31;
+    double aux = 0.0;
+#pragma unroll 1
+    for (int t = warp; t < p.T; t += 4) {
+        float v[kFewMaxN / 32];
+        few_logits(p, t, lane, v);
+        const float top = __ldcg(p.logits + (int64_t)t * p.N + s.expert[t * p.k]);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kFewMaxN / 32; ++i) {
+            if (32 * i >= p.N) break;
+            v[i] = 32 * i + lane < p.N ? expf(v[i] - top) : 0.f;
+            sum += v[i];
         }
-        p.y[(int64_t)t * p.d + row] = y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane < p.k) {
+            const float l = __ldcg(p.logits + (int64_t)t * p.N + s.expert[t * p.k + lane]);
+            s.gate[t * p.k + lane] = expf(l - top) / sum;  // NaN for a token whose logits are not finite
+        }
+        if (outputs) {
+#pragma unroll
+            for (int i = 0; i < kFewMaxN / 32; ++i) {
+                if (32 * i >= p.N) break;
+                const int f = 32 * i + lane < p.N ? s.first[32 * i + lane] : 0;
+                if (f) aux += (double)f * (double)(v[i] / sum);
+            }
+        }
     }
+    if (outputs) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) aux += __shfl_xor_sync(0xffffffffu, aux, o);
+        if (lane == 0) s.aux[warp] = aux;
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (outputs) {
+        for (int i = tid; i < p.T * p.k; i += 128)
+            p.expert[i] = s.expert[i], p.gate[i] = s.gate[i], p.slot[i] = s.slot[i];
+        for (int n = tid; n < p.N; n += 128) p.counts[n] = s.cnt[n];
+        if (tid == 0)
+            *p.aux = (float)(((s.aux[0] + s.aux[1]) + (s.aux[2] + s.aux[3])) * (double)p.N / ((double)p.T * p.T));
+    }
+}
+
+__device__ __forceinline__ int32_t atom_add_acq_rel_gpu(int32_t *p, int32_t v) {
+    int32_t old;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
 }
 
 }  // namespace switchmoe

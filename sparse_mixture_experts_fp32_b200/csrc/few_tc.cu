@@ -87,14 +87,13 @@ __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[
 }
 
 // Parts that the length of a product is cut into: the least of (waves of
-// items) x (stages of an item + 2 for its epilogue and hand-over).
-__device__ __forceinline__ int few_splits(int tiles, int stages, int max_splits, int blocks) {
-    int best = 1, cost = ((tiles + blocks - 1) / blocks) * (stages + 2);
-    for (int s = 2; s <= max_splits && s <= stages; s *= 2) {
-        const int c = ((tiles * s + blocks - 1) / blocks) * ((stages + s - 1) / s + 2);
-        if (c < cost) best = s, cost = c;
-    }
-    return best;
+// items) x (stages of an item + 1 for its epilogue and hand-over), in half
+// stages.  Lane l of the warp weighs 2^l parts.
+__device__ __forceinline__ int few_splits(int tiles, int stages, int max_splits, int blocks, int lane) {
+    const int s = 1 << (lane & 7);
+    const bool can = s <= max_splits && s <= stages;
+    const uint32_t cost = can ? (uint32_t)((tiles * s + blocks - 1) / blocks) * (2 * ((stages + s - 1) / s) + 1) : 0xffffffu;
+    return 1 << (__reduce_min_sync(0xffffffffu, min(cost, 0xffffffu) << 3 | (lane & 7)) & 7);
 }
 
 // Work of the call, the same in every block.
@@ -246,7 +245,7 @@ __device__ __forceinline__ void build_h(const FewArgs &p, uint8_t *tile, int A, 
         if (at < p.F) {
             const float *src = p.h + (int64_t)(a0 + tok) * p.F + at;
             const int64_t step = (int64_t)A * p.F;
-#pragma unroll 2
+#pragma unroll 4
             for (int q = 0; q < splits; ++q) {
 #pragma unroll
                 for (int j = 0; j < V / 4; ++j) add4(v + 4 * j, src + q * step + 4 * j);
@@ -300,33 +299,34 @@ __device__ __forceinline__ void add_accumulator(uint32_t taddr, int m, float (&v
     }
 }
 
-// y of one output row for every token.
-__device__ __forceinline__ void combine_row(const FewArgs &p, const FewPlan &s, int splits, int A, int row) {
+// y of one output row for the group's tokens in `mask`, whose parts are all there.
+__device__ __forceinline__ void combine_row(const FewArgs &p, const FewPlan &s, int splits, int A, int a0,
+                                            uint32_t mask, int row) {
     const int64_t step = (int64_t)A * p.d;
-    if (splits == 1) {
-#pragma unroll 4
-        for (int t = 0; t < p.T; ++t) {
-            float y = 0.f;
-            for (int c = 0; c < p.k; ++c) {
-                const int a = s.pos[t * p.k + c];
-                const float o = __ldcg(p.o + (int64_t)max(a, 0) * p.d + row);
-                if (a >= 0) y += s.gate[t * p.k + c] * o;
-            }
-            p.y[(int64_t)t * p.d + row] = y;
+    while (mask) {  // four tokens at a time, their loads in flight together
+        int t[4];
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            t[u] = s.token[a0 + __ffs(mask) - 1];  // past the last one: the last one again
+            if (mask & (mask - 1)) mask &= mask - 1;
+            else if (u == 3) mask = 0;
         }
-    } else {
-        for (int t = 0; t < p.T; ++t) {
-            float y = 0.f;
-            for (int c = 0; c < p.k; ++c) {
-                const int a = s.pos[t * p.k + c];
-                if (a < 0) continue;
-                float o = 0.f;
+        for (int c = 0; c < p.k; ++c) {
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
+            const float *src[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) src[u] = p.o + (int64_t)max(s.pos[t[u] * p.k + c], 0) * p.d + row;
 #pragma unroll 4
-                for (int q = 0; q < splits; ++q) o += __ldcg(p.o + q * step + (int64_t)a * p.d + row);
-                y += s.gate[t * p.k + c] * o;
-            }
-            p.y[(int64_t)t * p.d + row] = y;
+            for (int q = 0; q < splits; ++q)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) o[u] += __ldcg(src[u] + q * step);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (s.pos[t[u] * p.k + c] >= 0) y[u] += s.gate[t[u] * p.k + c] * o[u];
         }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) p.y[(int64_t)t[u] * p.d + row] = y[u];
     }
 }
 
@@ -376,8 +376,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     w.tiles_o = (p.d + 127) / 128;
     w.len_h = (p.d * (E4M3 ? 1 : 2) + 127) / 128;
     w.len_o = (p.F * (E4M3 ? 1 : 2) + 127) / 128;
-    w.splits_h = few_splits(w.groups * w.tiles_h, w.len_h, max_splits, gridDim.x);
-    w.splits_o = few_splits(w.groups * w.tiles_o, w.len_o, max_splits, gridDim.x);
+    w.splits_h = few_splits(w.groups * w.tiles_h, w.len_h, max_splits, gridDim.x, lane);
+    w.splits_o = few_splits(w.groups * w.tiles_o, w.len_o, max_splits, gridDim.x, lane);
     w.items_h = w.groups * w.tiles_h * w.splits_h;
     w.items = w.items_h + w.groups * w.tiles_o * w.splits_o;
     // The ring and the accumulators are laid out for the call's largest group:
@@ -476,6 +476,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else if (warp < 6) {
         const int quarter = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        // while the first weights are on their way
+        few_gates(p, s.plan, tid - 64, blockIdx.x == 0);
+        for (int t = blockIdx.x; t < p.T; t += gridDim.x)  // tokens that no expert keeps
+            if (s.plan.pos[t * p.k] < 0 && s.plan.pos[t * p.k + p.k - 1] < 0)
+                for (int j = tid - 64; j < p.d; j += 128) p.y[(int64_t)t * p.d + j] = 0.f;
+        const bool direct = p.k == 1 && w.splits_o == 1;  // an item's output rows are y's
         int buf = 0;
         uint32_t acc_phase = 0, n = 0;
         bool ok = true;
@@ -532,18 +538,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (lane == 0) atomicMax(p.hmax + it.split * A + a0 + j, top);
                     }
                 }
-                if (live) out[(int64_t)j * rows + row] = u;
+                if (live) {
+                    if (it.second && direct) {
+                        const int t = s.plan.token[a0 + j];
+                        p.y[(int64_t)t * p.d + row] = s.plan.gate[t] * u;
+                    } else {
+                        out[(int64_t)j * rows + row] = u;
+                    }
+                }
             }
             __syncwarp();
-            int last = 0;
-            if (lane == 0) {
-                __threadfence();
-                if (it.second)
-                    last = atomicAdd(&p.ctr->tile[it.tile * 4 + quarter], 1) == w.groups * w.splits_o - 1;
-                else red_release_add_gpu(&p.ctr->done[it.g], 1);
-                __threadfence();
+            if (!it.second) {
+                if (lane == 0) red_release_add_gpu(&p.ctr->done[it.g], 1);
+            } else if (!direct) {  // the warp that stores the last part of a token's values forms them
+                bool last = false;
+                if (lane < m) {
+                    const int t = s.plan.token[a0 + lane];
+                    const int kept = (s.plan.pos[t * p.k] >= 0) + (p.k == 2 && s.plan.pos[t * p.k + 1] >= 0);
+                    last = atom_add_acq_rel_gpu(p.parts + (int64_t)(it.tile * 4 + quarter) * p.T + t, 1) ==
+                           kept * w.splits_o - 1;
+                }
+                const uint32_t mask = __ballot_sync(0xffffffffu, last);
+                if (mask && live) combine_row(p, s.plan, w.splits_o, A, a0, mask, row);
+                __syncwarp();
             }
-            if (__shfl_sync(0xffffffffu, last, 0) && live) combine_row(p, s.plan, w.splits_o, A, row);
         }
     } else {
         // No more builders than stages: one that is a whole lap of the ring ahead of
@@ -599,6 +617,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
     }
+    pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
