@@ -534,6 +534,8 @@ def _want(name, t, shape, dtypes, device):
     """Checks an argument and returns its pointer (None for None)."""
     if t is None:
         return None
+    if t.shape == shape and t.dtype in dtypes and t.device == device and t.is_contiguous() and t.is_cuda:
+        return t.data_ptr()
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype not in dtypes:
@@ -561,14 +563,21 @@ def _result(out, key, make):
 def _launch(fn, where, device, *args):
     """Calls the C function on the current stream of `device`, which is made current meanwhile."""
     import torch
-    stream = torch.cuda.current_stream(device).cuda_stream
     if torch.cuda.current_device() == device.index:
-        status = fn(*args, stream)
+        status = fn(*args, _current_stream(device))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, stream)
+            status = fn(*args, _current_stream(device))
     if status != 0:
         raise SwitchError(status, where)
+
+
+def _current_stream(device) -> int:
+    """The current stream of `device` as a cudaStream_t, without the torch.cuda.Stream object around it (2 us of a
+    call that takes 10) where torch gives it so."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _under(stream, device):
@@ -618,8 +627,10 @@ def norm_fwd(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None, in
         out["sum"] = residual
     d = SwitchNormDims(T, dm, dtype_code(residual.dtype), SWITCH_F32 if delta is None else dtype_code(delta.dtype),
                        _code(out_dtype), eps)
-    _launch(lib().switch_norm_fwd, "switch_norm_fwd", dev, ctypes.byref(d), pr, pd, pw, _ptr(out["sum"]),
-            _ptr(out["out"]), _ptr(out["scale"]), _ptr(out["rstd"]))
+    total, scale = out["sum"], out["scale"]
+    _launch(lib().switch_norm_fwd, "switch_norm_fwd", dev, ctypes.byref(d), pr, pd, pw,
+            None if total is None else total.data_ptr(), out["out"].data_ptr(),
+            None if scale is None else scale.data_ptr(), out["rstd"].data_ptr())
     return out
 
 
@@ -643,7 +654,7 @@ def norm_bwd(sum, weight, rstd, dout, dsum=None, out=None, stream=None):
     size = switch_norm_workspace_size(d)
     ws = torch.empty(size, dtype=torch.uint8, device=dev)
     _launch(lib().switch_norm_bwd, "switch_norm_bwd", dev, ctypes.byref(d), ps, pw, pr, pg, pu,
-            _ptr(out["dresidual"]), _ptr(out["dweight"]), ws.data_ptr(), size)
+            out["dresidual"].data_ptr(), out["dweight"].data_ptr(), ws.data_ptr(), size)
     return out
 
 
@@ -663,11 +674,11 @@ def quantize_rows(x, out=None, stream=None):
     for n in x.shape[:-1]:
         rows *= n
     px = _want("x", x, x.shape, (torch.float32, torch.bfloat16), dev)
-    out = _result(out, ("quantize_rows", tuple(x.shape), dev), lambda: dict(
+    out = _result(out, ("quantize_rows", x.shape, dev), lambda: dict(
         q=torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev),
         scale=torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)))
     _launch(lib().switch_quantize_rows, "switch_quantize_rows", dev, rows, cols, dtype_code(x.dtype), px,
-            _ptr(out["q"]), _ptr(out["scale"]))
+            out["q"].data_ptr(), out["scale"].data_ptr())
     return out
 
 

@@ -62,12 +62,14 @@ __device__ __forceinline__ void load_elems(const T *p, float (&v)[V]) {
 // ---------------------------------------------------------------------------
 // router
 // ---------------------------------------------------------------------------
-constexpr int kRouterThreads = 256;
+// Four warps of 64 registers: a block fits beside one of the second kernel's on an SM, so that those
+// start, and the next call's routers with them, before the others end.
+constexpr int kRouterThreads = 128;
 
 // Block (i, j): the logits of TE experts for TT tokens, the dot products
 // spread over the block's threads, V elements each; sums in a fixed order.
 template <typename X, int V, int TE, int TT>
-__global__ void __launch_bounds__(kRouterThreads)
+__global__ void __launch_bounds__(kRouterThreads, 8)
     few_router_kernel(const FewArgs p, int zero_ints, int want_xmax) {
     __shared__ float red[kRouterThreads / 32][TE * TT];
     __shared__ uint32_t big[kRouterThreads / 32][TT];
@@ -97,7 +99,7 @@ __global__ void __launch_bounds__(kRouterThreads)
         for (int e = 0; e < TE; ++e) acc[e][t] = 0.f;
     }
     // several steps' loads in flight: rows of W_r come from memory, 1 us away
-#pragma unroll(TE * TT == 1 ? 8 : TE == 1 ? 4 : 2)
+#pragma unroll(TE * TT == 1 ? 8 : TE == 1 ? 2 : 1)
     for (int j = tid * V; j < p.d; j += kRouterThreads * V) {
         float wv[TE][V];
 #pragma unroll
@@ -159,14 +161,15 @@ template <typename X, int V>
 cudaError_t router_typed(const FewArgs &p, int zero_ints, int want_xmax, cudaStream_t stream) {
     // one expert per block for the most blocks in flight; with many blocks four, so that a row of x serves four
     if (p.T == 1) return router_launch<X, V, 1, 1>(p, zero_ints, want_xmax, stream);
-    if (p.N * ((p.T + 7) / 8) <= 592) return router_launch<X, V, 1, 8>(p, zero_ints, want_xmax, stream);
-    return router_launch<X, V, 4, 8>(p, zero_ints, want_xmax, stream);
+    if (p.N * ((p.T + 3) / 4) <= 1184) return router_launch<X, V, 1, 4>(p, zero_ints, want_xmax, stream);
+    return router_launch<X, V, 4, 4>(p, zero_ints, want_xmax, stream);
 }
 
 // ---------------------------------------------------------------------------
 // experts on CUDA cores
 // ---------------------------------------------------------------------------
 constexpr int kSimtThreads = 256;
+constexpr int kSimtBlocks = 2;  // per SM
 constexpr int kSimtWarps = kSimtThreads / 32;
 constexpr int kSimtRows = 8;    // weight rows of an item
 constexpr int kSimtTokens = 8;  // tokens of a group
@@ -221,7 +224,7 @@ __device__ __forceinline__ void simt_dots(const W *w, int64_t rows_left, int K, 
 }
 
 template <typename W, typename X, int V>
-__global__ void __launch_bounds__(kSimtThreads) few_experts_simt_kernel(const FewArgs p) {
+__global__ void __launch_bounds__(kSimtThreads, kSimtBlocks) few_experts_simt_kernel(const FewArgs p) {
     __shared__ SimtShared s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();  // the logits and the zeroed counters
@@ -306,12 +309,8 @@ __global__ void __launch_bounds__(kSimtThreads) few_experts_simt_kernel(const Fe
 
 template <typename W, typename X, int V>
 cudaError_t experts_simt(const FewArgs &p, cudaStream_t stream) {
-    int per_sm = 0;
-    cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, few_experts_simt_kernel<W, X, V>,
-                                                                    kSimtThreads, 0);
-    if (err != cudaSuccess) return err;
-    return launch_kernel(few_experts_simt_kernel<W, X, V>, dim3(device_sm_count() * (per_sm < 1 ? 1 : per_sm)),
-                         dim3(kSimtThreads), 0, stream, true, p);
+    return launch_kernel(few_experts_simt_kernel<W, X, V>, dim3(device_sm_count() * kSimtBlocks), dim3(kSimtThreads), 0,
+                         stream, true, p);
 }
 
 }  // namespace

@@ -49,10 +49,13 @@ struct FewPlan {
     int slot[kFewMaxA];      // [t * k + c], -1: dropped
     int pos[kFewMaxA];       // [t * k + c] -> position, -1: dropped
     int token[kFewMaxA];     // [position] -> token
-    uint32_t order[kFewMaxA / 4];  // expert of every pair, a byte each, first choices before second ones
-    int cnt[kFewMaxN], first[kFewMaxN], base[kFewMaxN];  // pairs, first choices, first position of each expert
+    // an entry per pair, first choices (in token order) before second ones
+    uint32_t order[kFewMaxA / 4];  // its expert, a byte each
+    uint32_t keeps[kFewMaxA / 4];  // 0xff where it is kept
+    int lead[kFewMaxA];      // [position] size of the group that begins there, 0: none does
+    int lead_expert[kFewMaxA];
     int g_expert[kFewMaxA], g_first[kFewMaxA], g_size[kFewMaxA];
-    int part[kFewMaxN / 32];
+    int cnt[kFewMaxN], first[kFewMaxN];  // pairs and first choices of each expert (the block that writes the outputs)
     double aux[4];
     int groups, largest;     // groups; positions of the largest one
 };
@@ -99,15 +102,15 @@ __device__ __forceinline__ int few_argmax(const uint32_t (&key)[kFewMaxN / 32], 
 __device__ inline void few_plan(const FewArgs &p, FewPlan &s, int group_max, int threads) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = threads >> 5;
     const int A = p.T * p.k;
-    for (int n = tid; n < p.N; n += threads) s.cnt[n] = s.first[n] = 0;
-    if (tid == 0) s.largest = 0;
+    if (tid < kFewMaxA) s.lead[tid] = 0;
+    float v[kFewMaxN / 32];
+    if (warp < p.T) few_logits(p, warp, lane, v);
 #pragma unroll 1
     for (int t = warp; t < p.T; t += warps) {
-        float v[kFewMaxN / 32];
-        few_logits(p, t, lane, v);
         uint32_t key[kFewMaxN / 32];
 #pragma unroll
         for (int i = 0; i < kFewMaxN / 32; ++i) key[i] = ordered_bits(v[i]);
+        if (t + warps < p.T) few_logits(p, t + warps, lane, v);
         const int first = few_argmax(key, p.N, -1, lane);
         const int second = p.k == 2 ? few_argmax(key, p.N, first, lane) : 0;
         if (lane == 0) {
@@ -120,54 +123,66 @@ __device__ inline void few_plan(const FewArgs &p, FewPlan &s, int group_max, int
         }
     }
     __syncthreads();
-    for (int i = tid; i < A; i += threads) {  // rank among the pairs of its expert; first choices come first
-        const int c = i >= p.T, t = c ? i - p.T : i, e = s.expert[t * p.k + c];
+    // Entry i: the entries of its expert before it (its rank, its slot where it is kept), of its expert, and of
+    // lower experts; four at a time.
+    const bool mine = tid < A;
+    const int c = tid >= p.T, t = c ? tid - p.T : tid;
+    int e = 0, rank = 0, same = 0, lower = 0;
+    if (mine) {
+        e = s.expert[t * p.k + c];
         const uint32_t four = (uint32_t)e * 0x01010101u;
-        int rank = 0;
-#pragma unroll 4
-        for (int w = 0; w < i / 4; ++w) rank += __popc(__vcmpeq4(s.order[w], four)) >> 3;
-        if (i & 3) rank += __popc(__vcmpeq4(s.order[i >> 2], four) & ((1u << (8 * (i & 3))) - 1u)) >> 3;
-        s.slot[t * p.k + c] = rank < p.C ? rank : -1;
-        atomicAdd(&s.cnt[e], 1);
-        if (c == 0) atomicAdd(&s.first[e], 1);
+#pragma unroll 2
+        for (int w = 0; 4 * w < A; ++w) {
+            const uint32_t valid = A - 4 * w >= 4 ? 0xffffffffu : (1u << (8 * (A - 4 * w))) - 1u;
+            const uint32_t before = 4 * w + 4 <= tid ? 0xffffffffu : 4 * w < tid ? (1u << (8 * (tid - 4 * w))) - 1u : 0u;
+            const uint32_t eq = __vcmpeq4(s.order[w], four) & valid;
+            same += __popc(eq) >> 3;
+            rank += __popc(eq & before) >> 3;
+            lower += __popc(__vcmpltu4(s.order[w], four) & valid) >> 3;
+        }
+    }
+    const bool keep = mine && rank < p.C;
+    if (p.C < p.T) {  // some may be dropped: count the kept ones of lower experts again
+        if (mine) reinterpret_cast<uint8_t *>(s.keeps)[tid] = keep ? 0xff : 0;
+        __syncthreads();
+        if (keep) {
+            const uint32_t four = (uint32_t)e * 0x01010101u;
+            lower = 0;
+            for (int w = 0; 4 * w < A; ++w) {
+                const uint32_t valid = A - 4 * w >= 4 ? 0xffffffffu : (1u << (8 * (A - 4 * w))) - 1u;
+                lower += __popc(__vcmpltu4(s.order[w], four) & s.keeps[w] & valid) >> 3;
+            }
+        }
+    }
+    if (mine) {
+        s.slot[t * p.k + c] = keep ? rank : -1;
+        s.pos[t * p.k + c] = keep ? lower + rank : -1;
+        if (keep) {
+            s.token[lower + rank] = t;
+            if (rank % group_max == 0) {
+                s.lead[lower + rank] = min(group_max, min(same, p.C) - rank);
+                s.lead_expert[lower + rank] = e;
+            }
+        }
     }
     __syncthreads();
-    int kept = 0, mine = 0, run = 0;
-    if (warp < kFewMaxN / 32) {  // positions (low half) and groups (high half) before each expert
-        kept = tid < p.N ? min(s.cnt[tid], p.C) : 0;
-        mine = (kept + group_max - 1) / group_max;
-        run = kept | mine << 16;
+    if (warp == 0) {
+        int groups = 0, largest = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, run, o);
-            if (lane >= o) run += u;
+        for (int q = 0; q < kFewMaxA / 32; ++q) {
+            const int a = 32 * q + lane, size = s.lead[a];
+            const uint32_t leads = __ballot_sync(0xffffffffu, size > 0);
+            if (size > 0) {
+                const int g = groups + __popc(leads & ((1u << lane) - 1u));
+                s.g_expert[g] = s.lead_expert[a];
+                s.g_first[g] = a;
+                s.g_size[g] = size;
+            }
+            groups += __popc(leads);
+            largest = max(largest, size);
         }
-        if (lane == 31) s.part[warp] = run;
-        const int largest = __reduce_max_sync(0xffffffffu, min(kept, group_max));
-        if (lane == 0) atomicMax(&s.largest, largest);
-    }
-    __syncthreads();
-    if (warp < kFewMaxN / 32) {
-        int all = 0;
-#pragma unroll
-        for (int q = 0; q < kFewMaxN / 32; ++q) {
-            if (q < warp) run += s.part[q];
-            all += s.part[q];
-        }
-        const int a = (run & 0xffff) - kept, g = (run >> 16) - mine;
-        if (tid < p.N) s.base[tid] = a;
-        for (int j = 0; j < mine; ++j) {
-            s.g_expert[g + j] = tid;
-            s.g_first[g + j] = a + j * group_max;
-            s.g_size[g + j] = min(group_max, kept - j * group_max);
-        }
-        if (tid == 0) s.groups = all >> 16;
-    }
-    __syncthreads();
-    for (int i = tid; i < A; i += threads) {
-        const int at = s.slot[i] < 0 ? -1 : s.base[s.expert[i]] + s.slot[i];
-        s.pos[i] = at;
-        if (at >= 0) s.token[at] = p.k == 2 ? i >> 1 : i;
+        largest = __reduce_max_sync(0xffffffffu, largest);
+        if (lane == 0) s.groups = groups, s.largest = largest;
     }
     __syncthreads();
 }
@@ -179,6 +194,15 @@ __device__ inline void few_plan(const FewArgs &p, FewPlan &s, int group_max, int
 __device__ inline void few_gates(const FewArgs &p, FewPlan &s, int tid, bool outputs) {
     const int warp = tid >> 5, lane = tid & 31;
     double aux = 0.0;
+    if (outputs) {
+        for (int n = tid; n < p.N; n += 128) s.cnt[n] = s.first[n] = 0;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        for (int i = tid; i < p.T * p.k; i += 128) {
+            atomicAdd(&s.cnt[s.expert[i]], 1);
+            if (p.k == 1 || (i & 1) == 0) atomicAdd(&s.first[s.expert[i]], 1);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
 #pragma unroll 1
     for (int t = warp; t < p.T; t += 4) {
         float v[kFewMaxN / 32];

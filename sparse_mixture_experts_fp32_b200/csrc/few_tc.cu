@@ -32,6 +32,8 @@
 // equal parts when there are few tiles (few_splits).
 #include <cuda.h>
 
+#include <atomic>
+
 #include "few.cuh"
 
 namespace switchmoe {
@@ -62,7 +64,7 @@ struct TcShared {
     uint64_t drain;
     uint32_t tmem;
     int queue[kQueue];
-    int splits_h, splits_o;
+    int ready[kFewMaxA];  // groups whose first product is complete
 };
 
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -89,16 +91,17 @@ __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[
 // Parts that the length of a product is cut into: the least of (waves of
 // items) x (stages of an item + 1 for its epilogue and hand-over), in half
 // stages.  Lane l of the warp weighs 2^l parts.
-__device__ __forceinline__ int few_splits(int tiles, int stages, int max_splits, int blocks, int lane) {
-    const int s = 1 << (lane & 7);
-    const bool can = s <= max_splits && s <= stages;
-    const uint32_t cost = can ? (uint32_t)((tiles * s + blocks - 1) / blocks) * (2 * ((stages + s - 1) / s) + 1) : 0xffffffu;
-    return 1 << (__reduce_min_sync(0xffffffffu, min(cost, 0xffffffu) << 3 | (lane & 7)) & 7);
+// Returned as a power of two's exponent.
+__device__ __forceinline__ int few_splits(int tiles, int stages, int max_splits, float blocks, int lane) {
+    const int log = lane & 7, s = 1 << log;
+    const uint32_t waves = (uint32_t)__fdividef((float)(tiles * s) + blocks - 1.f, blocks);
+    const uint32_t cost = s <= max_splits && s <= stages ? waves * (2 * ((stages + s - 1) >> log) + 1) : 0xffffffu;
+    return (int)(__reduce_min_sync(0xffffffffu, min(cost, 0xffffffu) << 3 | log) & 7);
 }
 
 // Work of the call, the same in every block.
 struct Work {
-    int groups, tiles_h, tiles_o, len_h, len_o, splits_h, splits_o, items_h, items;
+    int groups, tiles_h, tiles_o, len_h, len_o, log_h, log_o, splits_h, splits_o, items_h, items;
 };
 struct Item {
     bool second;
@@ -108,22 +111,43 @@ __device__ __forceinline__ Item locate(const Work &w, int item) {
     Item it;
     it.second = item >= w.items_h;
     if (!it.second) {
-        it.split = item % w.splits_h;
-        const int q = item / w.splits_h;
-        it.tile = q % w.tiles_h;
+        it.split = item & (w.splits_h - 1);
+        const int q = item >> w.log_h;
         it.g = q / w.tiles_h;
-        it.k0 = it.split * w.len_h / w.splits_h;
-        it.k1 = (it.split + 1) * w.len_h / w.splits_h;
+        it.tile = q - it.g * w.tiles_h;
+        it.k0 = it.split * w.len_h >> w.log_h;
+        it.k1 = (it.split + 1) * w.len_h >> w.log_h;
     } else {  // all groups' parts of a tile of output rows follow one another
-        const int r = item - w.items_h;
-        it.g = r % w.groups;
-        const int q = r / w.groups;
-        it.split = q % w.splits_o;
-        it.tile = q / w.splits_o;
-        it.k0 = it.split * w.len_o / w.splits_o;
-        it.k1 = (it.split + 1) * w.len_o / w.splits_o;
+        const int r = item - w.items_h, q = r / w.groups;
+        it.g = r - q * w.groups;
+        it.split = q & (w.splits_o - 1);
+        it.tile = q >> w.log_o;
+        it.k0 = it.split * w.len_o >> w.log_o;
+        it.k1 = (it.split + 1) * w.len_o >> w.log_o;
     }
     return it;
+}
+
+// A flag in shared memory that one thread of the block sets once (release) and others read (acquire).
+__device__ __forceinline__ bool ready_cta(const int *flag) {
+    int v;
+    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(smem_u32(flag)) : "memory");
+    return v != 0;
+}
+__device__ __forceinline__ void set_ready_cta(int *flag) {
+    asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(flag)), "r"(1) : "memory");
+}
+__device__ __forceinline__ bool wait_ready_cta(const int *flag, DeviceStatus *st, int32_t where) {
+    if (ready_cta(flag)) return true;
+    const uint64_t start = global_ns();
+    while (!ready_cta(flag)) {
+        __nanosleep(20);
+        if (global_ns() - start > kWaitLimitNs) {
+            report_status(st, SWITCH_ERR_DEVICE_TIMEOUT, where);
+            return false;
+        }
+    }
+    return true;
 }
 
 // Next item from the queue, for one warp; -1: no more, or a wait gave up.
@@ -361,7 +385,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
         tmem_alloc(&s.tmem, 512);
         tmem_relinquish();
+        tc_fence_before();
     }
+    if (tid < kFewMaxA) s.ready[tid] = 0;
     if (tid == 0) {
         prefetch_tmap(&tmap_in);
         prefetch_tmap(&tmap_out);
@@ -376,10 +402,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     w.tiles_o = (p.d + 127) / 128;
     w.len_h = (p.d * (E4M3 ? 1 : 2) + 127) / 128;
     w.len_o = (p.F * (E4M3 ? 1 : 2) + 127) / 128;
-    w.splits_h = few_splits(w.groups * w.tiles_h, w.len_h, max_splits, gridDim.x, lane);
-    w.splits_o = few_splits(w.groups * w.tiles_o, w.len_o, max_splits, gridDim.x, lane);
-    w.items_h = w.groups * w.tiles_h * w.splits_h;
-    w.items = w.items_h + w.groups * w.tiles_o * w.splits_o;
+    w.log_h = few_splits(w.groups * w.tiles_h, w.len_h, max_splits, (float)gridDim.x, lane);
+    w.log_o = few_splits(w.groups * w.tiles_o, w.len_o, max_splits, (float)gridDim.x, lane);
+    w.splits_h = 1 << w.log_h;
+    w.splits_o = 1 << w.log_o;
+    w.items_h = w.groups * w.tiles_h << w.log_h;
+    w.items = w.items_h + (w.groups * w.tiles_o << w.log_o);
     // The ring and the accumulators are laid out for the call's largest group:
     // bytes of a stage's column operand (whole 8-row swizzle atoms), stages, columns and number of accumulators.
     constexpr int kTerms = Terms<E4M3, X8>::second;  // the larger of the two products'
@@ -388,9 +416,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int acc_cols = ((s.plan.largest + 7) / 8 * 8 * kTerms + 31) / 32 * 32;
     const int bufs = min(512 / acc_cols, kMaxBufs);
     uint8_t *ring_b = ring_a + stages * kStageA;
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
+    tc_fence_after();  // the plan's barriers stand between the allocation and here
     const uint32_t tmem = s.tmem;
 
     if (warp == 0) {
@@ -576,19 +602,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (item < 0) break;
             const Item it = locate(w, item);
             const int a0 = s.plan.g_first[it.g], m = s.plan.g_size[it.g];
+            // One warp of the block asks memory whether the group's first product is complete, the others that one.
+            if (it.second && !ready_cta(&s.ready[it.g])) {
+                int fine = 1;
+                if (lane == 0) {
+                    if (me == 0) {
+                        fine = wait_counter_geq(&p.ctr->done[it.g], 4 * w.tiles_h << w.log_h, p.status, 91);
+                        if (fine) set_ready_cta(&s.ready[it.g]);
+                    } else {
+                        fine = wait_ready_cta(&s.ready[it.g], p.status, 93);
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, fine, 0) != 0;
+                if (!ok) break;
+            }
             int my_exp = 0;  // 8-bit experts: exponent of token `lane`'s scale
             bool ready = false;
             for (int kc = it.k0; kc < it.k1; ++kc, ++count) {
                 if (count % builders == me) {
                     if (!ready) {
                         ready = true;
-                        if (it.second) {
-                            int fine = 1;
-                            if (lane == 0)
-                                fine = wait_counter_geq(&p.ctr->done[it.g], 4 * w.tiles_h * w.splits_h, p.status, 91);
-                            ok = __shfl_sync(0xffffffffu, fine, 0) != 0;
-                            if (!ok) break;
-                        }
                         if constexpr (E4M3) {
                             if (lane < m) {
                                 if (it.second) {
@@ -660,9 +693,17 @@ cudaError_t experts_tc(const FewArgs &p, int max_splits, cudaStream_t stream) {
     CUtensorMap in, out;
     if (!weight_map(&in, p.w_in, p.N, p.F, p.d, E4M3) || !weight_map(&out, p.w_out, p.N, p.d, p.F, E4M3))
         return cudaErrorInvalidValue;
-    const cudaError_t err = cudaFuncSetAttribute(few_experts_tc_kernel<E4M3, X8>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kRing);
+    static std::atomic<uint64_t> raised{0};  // devices whose limit is raised already, a bit each
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(raised.load(std::memory_order_relaxed) & bit)) {
+        err = cudaFuncSetAttribute(few_experts_tc_kernel<E4M3, X8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   1024 + kRing);
+        if (err != cudaSuccess) return err;
+        raised.fetch_or(bit, std::memory_order_relaxed);
+    }
     return launch_kernel(few_experts_tc_kernel<E4M3, X8>, dim3(device_sm_count()), dim3(kTcThreads), 1024 + kRing,
                          stream, true, in, out, p, max_splits);
 }
