@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(kRouterThreads, 8)
     __shared__ uint32_t big[kRouterThreads / 32][TT];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int e0 = blockIdx.x * TE, t0 = blockIdx.y * TT;
-    pdl_wait();  // x; and the call before this one may still use the workspace
     pdl_launch_dependents();
+    pdl_wait();  // x; and the call before this one may still use the workspace
     {  // the second kernel's counters and maxima, and the status word
         const int blocks = gridDim.x * gridDim.y, me = blockIdx.y * gridDim.x + blockIdx.x;
         int32_t *z = reinterpret_cast<int32_t *>(p.ctr);
@@ -304,7 +304,6 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtBlocks) few_experts_simt_ke
         }
         __syncthreads();
     }
-    pdl_launch_dependents();
 }
 
 template <typename W, typename X, int V>

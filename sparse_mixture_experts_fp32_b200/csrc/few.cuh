@@ -74,24 +74,10 @@ __device__ __forceinline__ void few_logits(const FewArgs &p, int t, int lane, fl
     }
 }
 
-// Lowest index of the largest logit but expert `skip`'s, for a warp.
-__device__ __forceinline__ int few_argmax(const uint32_t (&key)[kFewMaxN / 32], int N, int skip, int lane) {
-    uint32_t best = 0;
-#pragma unroll
-    for (int i = 0; i < kFewMaxN / 32; ++i) {
-        if (32 * i >= N) break;
-        if (32 * i + lane < N && 32 * i + lane != skip) best = max(best, key[i]);
-    }
-    best = __reduce_max_sync(0xffffffffu, best);
-    int at = -1;
-#pragma unroll
-    for (int i = 0; i < kFewMaxN / 32; ++i) {
-        if (32 * i >= N || at >= 0) break;
-        const int n = 32 * i + lane;
-        const uint32_t hit = __ballot_sync(0xffffffffu, n < N && n != skip && key[i] == best);
-        if (hit) at = 32 * i + __ffs(hit) - 1;
-    }
-    return at;
+// Of a warp's keys: the largest, and the lowest index that has it.
+__device__ __forceinline__ int few_argmax(uint32_t key, int index) {
+    const uint32_t best = __reduce_max_sync(0xffffffffu, key);
+    return (int)__reduce_min_sync(0xffffffffu, key == best ? (uint32_t)index : 0xffffu);
 }
 
 // Every thread of a block of `threads` (a multiple of 32, at least 256) calls
@@ -102,17 +88,27 @@ __device__ __forceinline__ int few_argmax(const uint32_t (&key)[kFewMaxN / 32], 
 __device__ inline void few_plan(const FewArgs &p, FewPlan &s, int group_max, int threads) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = threads >> 5;
     const int A = p.T * p.k;
-    if (tid < kFewMaxA) s.lead[tid] = 0;
+    if (tid < kFewMaxA) {
+        s.lead[tid] = 0;
+        if (tid >= A) reinterpret_cast<uint8_t *>(s.order)[tid] = 0xff;
+    }
     float v[kFewMaxN / 32];
     if (warp < p.T) few_logits(p, warp, lane, v);
 #pragma unroll 1
     for (int t = warp; t < p.T; t += warps) {
-        uint32_t key[kFewMaxN / 32];
+        uint32_t k1 = 0, k2 = 0;  // this lane's two largest keys, the lower index first among equals
+        int n1 = 0xffff, n2 = 0xffff;
 #pragma unroll
-        for (int i = 0; i < kFewMaxN / 32; ++i) key[i] = ordered_bits(v[i]);
+        for (int i = 0; i < kFewMaxN / 32; ++i) {
+            if (32 * i >= p.N) break;
+            const int n = 32 * i + lane;
+            const uint32_t key = n < p.N ? ordered_bits(v[i]) : 0u;
+            if (n < p.N && (key > k1 || n1 == 0xffff)) k2 = k1, n2 = n1, k1 = key, n1 = n;
+            else if (n < p.N && (key > k2 || n2 == 0xffff)) k2 = key, n2 = n;
+        }
         if (t + warps < p.T) few_logits(p, t + warps, lane, v);
-        const int first = few_argmax(key, p.N, -1, lane);
-        const int second = p.k == 2 ? few_argmax(key, p.N, first, lane) : 0;
+        const int first = few_argmax(k1, n1);
+        const int second = p.k == 2 ? few_argmax(n1 == first ? k2 : k1, n1 == first ? n2 : n1) : 0;
         if (lane == 0) {
             s.expert[t * p.k] = first;
             reinterpret_cast<uint8_t *>(s.order)[t] = (uint8_t)first;
@@ -131,15 +127,17 @@ __device__ inline void few_plan(const FewArgs &p, FewPlan &s, int group_max, int
     if (mine) {
         e = s.expert[t * p.k + c];
         const uint32_t four = (uint32_t)e * 0x01010101u;
-#pragma unroll 2
+        // (a byte of a comparison is -1 where it holds; bytes past the last entry are 0xff)
+#pragma unroll 4
         for (int w = 0; 4 * w < A; ++w) {
-            const uint32_t valid = A - 4 * w >= 4 ? 0xffffffffu : (1u << (8 * (A - 4 * w))) - 1u;
-            const uint32_t before = 4 * w + 4 <= tid ? 0xffffffffu : 4 * w < tid ? (1u << (8 * (tid - 4 * w))) - 1u : 0u;
-            const uint32_t eq = __vcmpeq4(s.order[w], four) & valid;
-            same += __popc(eq) >> 3;
-            rank += __popc(eq & before) >> 3;
-            lower += __popc(__vcmpltu4(s.order[w], four) & valid) >> 3;
+            const uint32_t eq = __vcmpeq4(s.order[w], four);
+            const int n = -__dp4a((int)eq, 0x01010101, 0);
+            same += n;
+            if (4 * w + 4 <= tid) rank += n;
+            lower -= __dp4a((int)__vcmpltu4(s.order[w], four), 0x01010101, 0);
         }
+        if (tid & 3) rank += __popc(__vcmpeq4(s.order[tid >> 2], four) & ((1u << (8 * (tid & 3))) - 1u)) >> 3;
+        if (e == 255) same -= -A & 3;
     }
     const bool keep = mine && rank < p.C;
     if (p.C < p.T) {  // some may be dropped: count the kept ones of lower experts again
@@ -148,10 +146,8 @@ __device__ inline void few_plan(const FewArgs &p, FewPlan &s, int group_max, int
         if (keep) {
             const uint32_t four = (uint32_t)e * 0x01010101u;
             lower = 0;
-            for (int w = 0; 4 * w < A; ++w) {
-                const uint32_t valid = A - 4 * w >= 4 ? 0xffffffffu : (1u << (8 * (A - 4 * w))) - 1u;
-                lower += __popc(__vcmpltu4(s.order[w], four) & s.keeps[w] & valid) >> 3;
-            }
+            for (int w = 0; 4 * w < A; ++w)
+                lower -= __dp4a((int)(__vcmpltu4(s.order[w], four) & s.keeps[w]), 0x01010101, 0);
         }
     }
     if (mine) {
@@ -203,11 +199,22 @@ __device__ inline void few_gates(const FewArgs &p, FewPlan &s, int tid, bool out
         }
         asm volatile("bar.sync 1, 128;" ::: "memory");
     }
+    float v[kFewMaxN / 32], next[kFewMaxN / 32];
+    if (warp < p.T) few_logits(p, warp, lane, next);
 #pragma unroll 1
     for (int t = warp; t < p.T; t += 4) {
-        float v[kFewMaxN / 32];
-        few_logits(p, t, lane, v);
-        const float top = __ldcg(p.logits + (int64_t)t * p.N + s.expert[t * p.k]);
+        float top, l = 0.f;  // lane c: the logit of choice c
+        const int mine = s.expert[t * p.k + (lane < p.k ? lane : 0)];
+#pragma unroll
+        for (int i = 0; i < kFewMaxN / 32; ++i) v[i] = next[i];
+        if (t + 4 < p.T) few_logits(p, t + 4, lane, next);
+#pragma unroll
+        for (int i = 0; i < kFewMaxN / 32; ++i) {
+            if (32 * i >= p.N) break;
+            const float u = __shfl_sync(0xffffffffu, v[i], mine & 31);
+            if (mine >> 5 == i) l = u;
+        }
+        top = __shfl_sync(0xffffffffu, l, 0);
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < kFewMaxN / 32; ++i) {
@@ -217,10 +224,7 @@ __device__ inline void few_gates(const FewArgs &p, FewPlan &s, int tid, bool out
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane < p.k) {
-            const float l = __ldcg(p.logits + (int64_t)t * p.N + s.expert[t * p.k + lane]);
-            s.gate[t * p.k + lane] = expf(l - top) / sum;  // NaN for a token whose logits are not finite
-        }
+        if (lane < p.k) s.gate[t * p.k + lane] = expf(l - top) / sum;  // NaN for a token whose logits are not finite
         if (outputs) {
 #pragma unroll
             for (int i = 0; i < kFewMaxN / 32; ++i) {

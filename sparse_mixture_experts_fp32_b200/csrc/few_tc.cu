@@ -24,7 +24,7 @@
 //                 a ring of 16 KB stages
 //   warp 1        issues the MMAs
 //   warps 2-5     epilogue: 32 weight rows each
-//   warps 6-13    build the column operand of every eighth stage: gather x rows,
+//   warps 6-11    build the column operand of every sixth stage: gather x rows,
 //                 or add the partial sums of h, apply ReLU and cut into terms
 // The ring runs on across items and from the first product into the second:
 // weights of the second product are on their way while the first is finished.
@@ -45,7 +45,7 @@ constexpr int kMaxStages = 12;
 constexpr int kRing = 215 * 1024;  // of the 227 KB a block may have: the plan and the barriers take 8 KB
 constexpr int kMaxBufs = 8;
 constexpr int kChain = 4;         // stages per accumulator
-constexpr int kBuilders = 8;
+constexpr int kBuilders = 6;      // 4: 3 % slower (32 tokens), 8: 4 % slower (they leave 128 registers a thread)
 constexpr int kTcThreads = 32 * (6 + kBuilders);
 constexpr int kQueue = 4;
 constexpr int kConsumers = 1 + 4 + kBuilders;  // warps that read the item queue
@@ -252,33 +252,45 @@ __device__ __forceinline__ void build_x(const FewArgs &p, const FewPlan &s, uint
     }
 }
 
-// The column operand of stage `kc` of a second product: ReLU of the summed
-// parts of h, in terms.
+// V values of a pair's hidden row from `src` on: its parts summed in order.
+template <int V>
+__device__ __forceinline__ void load_h(const float *src, int64_t step, int splits, float (&v)[V]) {
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j) {
+        const float4 a = __ldcg(reinterpret_cast<const float4 *>(src) + j);
+        v[4 * j] = a.x, v[4 * j + 1] = a.y, v[4 * j + 2] = a.z, v[4 * j + 3] = a.w;
+    }
+#pragma unroll 4
+    for (int q = 1; q < splits; ++q)
+#pragma unroll
+        for (int j = 0; j < V / 4; ++j) add4(v + 4 * j, src + q * step + 4 * j);
+}
+
+// The column operand of stage `kc` of a second product: ReLU of h, in terms.
 template <bool E4M3>
 __device__ __forceinline__ void build_h(const FewArgs &p, uint8_t *tile, int A, int splits, int a0, int m, int kc,
                                         int my_exp, int lane) {
     constexpr int V = E4M3 ? 16 : 8;  // values per 16-byte chunk
-    const int tasks = m * 8;
-    for (int i0 = 0; i0 < tasks; i0 += 32) {
-        const int i = i0 + lane, tok = i >> 3, at = (kc * 8 + (i & 7)) * V;
-        const float up = E4M3 ? pow2(__shfl_sync(0xffffffffu, my_exp, tok & 31)) : 1.f;
-        if (i >= tasks) continue;
+    const int tasks = m * 8, at = (kc * 8 + (lane & 7)) * V;
+    const bool in = at < p.F;
+    const float *h = p.h + (int64_t)a0 * p.F + at;
+    const int64_t step = (int64_t)A * p.F;
+    float next[V];
+    int i = lane;
+    if (i < tasks && in) load_h<V>(h + (int64_t)(i >> 3) * p.F, step, splits, next);
+    for (int i0 = 0; i0 < tasks; i0 += 32, i += 32) {
         float v[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = 0.f;
-        if (at < p.F) {
-            const float *src = p.h + (int64_t)(a0 + tok) * p.F + at;
-            const int64_t step = (int64_t)A * p.F;
-#pragma unroll 4
-            for (int q = 0; q < splits; ++q) {
+        for (int j = 0; j < V; ++j) v[j] = next[j];
+        // the following task's values are on their way while this one's are cut
+        if (i + 32 < tasks && in) load_h<V>(h + (int64_t)((i + 32) >> 3) * p.F, step, splits, next);
+        const int tok = i >> 3;
+        const float up = E4M3 ? pow2(__shfl_sync(0xffffffffu, my_exp, tok & 31)) : 1.f;
+        if (i >= tasks) continue;
 #pragma unroll
-                for (int j = 0; j < V / 4; ++j) add4(v + 4 * j, src + q * step + 4 * j);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = v[j] < 0.f ? 0.f : v[j] * up;  // NaN stays NaN
+        for (int j = 0; j < V; ++j) v[j] = !in || v[j] < 0.f ? 0.f : v[j] * up;  // NaN stays NaN
         if constexpr (E4M3) {
-            store_e4m3_terms<5>(tile, tok * 5, i & 7, v);
+            store_e4m3_terms<5>(tile, tok * 5, lane & 7, v);
         } else {
             uint16_t t[3][8];
 #pragma unroll
@@ -293,7 +305,7 @@ __device__ __forceinline__ void build_h(const FewArgs &p, uint8_t *tile, int A, 
                 uint32_t w[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w[j] = (uint32_t)t[c][2 * j] | ((uint32_t)t[c][2 * j + 1] << 16);
-                *reinterpret_cast<uint4 *>(tile + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
+                *reinterpret_cast<uint4 *>(tile + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
                     make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
@@ -327,6 +339,21 @@ __device__ __forceinline__ void add_accumulator(uint32_t taddr, int m, float (&v
 __device__ __forceinline__ void combine_row(const FewArgs &p, const FewPlan &s, int splits, int A, int a0,
                                             uint32_t mask, int row) {
     const int64_t step = (int64_t)A * p.d;
+    if ((mask & (mask - 1)) == 0) {  // one token, its parts in flight together
+        const int t = s.token[a0 + __ffs(mask) - 1];
+        float y = 0.f;
+        for (int c = 0; c < p.k; ++c) {
+            const int a = s.pos[t * p.k + c];
+            if (a < 0) continue;
+            const float *src = p.o + (int64_t)a * p.d + row;
+            float o = 0.f;
+#pragma unroll 4
+            for (int q = 0; q < splits; ++q) o += __ldcg(src + q * step);
+            y += s.gate[t * p.k + c] * o;
+        }
+        p.y[(int64_t)t * p.d + row] = y;
+        return;
+    }
     while (mask) {  // four tokens at a time, their loads in flight together
         int t[4];
         float y[4] = {0.f, 0.f, 0.f, 0.f};
@@ -502,17 +529,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else if (warp < 6) {
         const int quarter = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-        // while the first weights are on their way
-        few_gates(p, s.plan, tid - 64, blockIdx.x == 0);
-        for (int t = blockIdx.x; t < p.T; t += gridDim.x)  // tokens that no expert keeps
-            if (s.plan.pos[t * p.k] < 0 && s.plan.pos[t * p.k + p.k - 1] < 0)
-                for (int j = tid - 64; j < p.d; j += 128) p.y[(int64_t)t * p.d + j] = 0.f;
         const bool direct = p.k == 1 && w.splits_o == 1;  // an item's output rows are y's
         int buf = 0;
         uint32_t acc_phase = 0, n = 0;
-        bool ok = true;
+        bool ok = true, gates = false;
+        // While the first weights are on their way; with at most one item of the first product per block
+        // between the products, when its last parts are on their way through other blocks.
+        const bool late = w.items_h <= (int)gridDim.x;
         while (ok) {
-            const int item = next_item(s, n, lane, p.status);
+            const int item = late || gates ? next_item(s, n, lane, p.status) : 0;
+            if (!gates && (!late || item < 0 || item >= w.items_h)) {
+                gates = true;
+                few_gates(p, s.plan, tid - 64, blockIdx.x == 0);
+                for (int t = blockIdx.x; t < p.T; t += gridDim.x)  // tokens that no expert keeps
+                    if (s.plan.pos[t * p.k] < 0 && s.plan.pos[t * p.k + p.k - 1] < 0)
+                        for (int j = tid - 64; j < p.d; j += 128) p.y[(int64_t)t * p.d + j] = 0.f;
+                if (!late) continue;
+            }
             if (item < 0) break;
             const Item it = locate(w, item);
             const int e = s.plan.g_expert[it.g], a0 = s.plan.g_first[it.g], m = s.plan.g_size[it.g];
@@ -590,8 +623,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
     } else {
-        // No more builders than stages: one that is a whole lap of the ring ahead of
-        // another would take the parity of an older phase for that of the one it waits for.
+        // No more builders than stages: the stages that a warp builds may not lie further apart than the
+        // ring is long, or it would take the parity of an older phase for that of the one it waits for.
         const int builders = min(kBuilders, stages), me = warp - 6;
         int stage = 0;
         uint32_t phase = 0, n = 0;
@@ -606,7 +639,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (it.second && !ready_cta(&s.ready[it.g])) {
                 int fine = 1;
                 if (lane == 0) {
-                    if (me == 0) {
+                    if (warp == 6) {
                         fine = wait_counter_geq(&p.ctr->done[it.g], 4 * w.tiles_h << w.log_h, p.status, 91);
                         if (fine) set_ready_cta(&s.ready[it.g]);
                     } else {
@@ -650,7 +683,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
     }
-    pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
