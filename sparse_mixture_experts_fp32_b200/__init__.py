@@ -524,10 +524,34 @@ def router_stats(result: dict, T: int, d_model: int, d_ff: int, dtype, stream=No
 # ---------------------------------------------------------------------------
 # residual + norm, 8-bit rows, the layer for a few tokens
 # ---------------------------------------------------------------------------
+class _Names:
+    """What the calls below need of torch, looked up once: a call of theirs is about as long as its Python."""
+
+    def __init__(self):
+        import torch
+        self.torch = torch
+        self.codes = {torch.float32: SWITCH_F32, torch.bfloat16: SWITCH_BF16, torch.float8_e4m3fn: SWITCH_E4M3}
+        self.f32, self.e4m3 = (torch.float32,), torch.float8_e4m3fn
+        self.floats = (torch.float32, torch.bfloat16)
+        self.current_device = torch.cuda.current_device
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a torch.cuda.Stream around it (2 us)
+        self.current_stream = raw if raw is not None else lambda i: torch.cuda.current_stream(i).cuda_stream
+
+
+_names = None
+
+
+def _torch_names() -> _Names:
+    global _names
+    if _names is None:
+        _names = _Names()
+    return _names
+
+
 def _code(dtype) -> int:
     """dtype_code with the 8-bit type (which only the calls below take)."""
-    import torch
-    return SWITCH_E4M3 if dtype == torch.float8_e4m3fn else dtype_code(dtype)
+    code = (_names or _torch_names()).codes.get(dtype)
+    return dtype_code(dtype) if code is None else code
 
 
 def _want(name, t, shape, dtypes, device):
@@ -546,38 +570,34 @@ def _want(name, t, shape, dtypes, device):
 
 
 class _Result(dict):
-    """A result that a later call of the same sizes may write into again (out=)."""
-    __slots__ = ("key",)
+    """A result that a later call of the same sizes may write into again (out=): the tensors of its first call,
+    whatever the dict holds by then."""
+    __slots__ = ("key", "own")
 
 
 def _result(out, key, make):
     """`out` when it came from a call with the same `key`, else new outputs (out=None) or an error."""
     if out is None:
-        out = _Result(make())
-        out.key = key
-    elif not isinstance(out, _Result) or out.key != key:
+        own = make()
+        out = _Result(own)
+        out.key, out.own = key, own
+    elif type(out) is not _Result or out.key != key:
         raise ValueError("out must be the result of an earlier call of the same function, sizes, types and device")
+    else:
+        out.update(out.own)
     return out
 
 
 def _launch(fn, where, device, *args):
     """Calls the C function on the current stream of `device`, which is made current meanwhile."""
-    import torch
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, _current_stream(device))
+    z, index = _names, device.index
+    if z.current_device() == index:
+        status = fn(*args, z.current_stream(index))
     else:
-        with torch.cuda.device(device):
-            status = fn(*args, _current_stream(device))
+        with z.torch.cuda.device(device):
+            status = fn(*args, z.current_stream(index))
     if status != 0:
         raise SwitchError(status, where)
-
-
-def _current_stream(device) -> int:
-    """The current stream of `device` as a cudaStream_t, without the torch.cuda.Stream object around it (2 us of a
-    call that takes 10) where torch gives it so."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _under(stream, device):
@@ -588,11 +608,13 @@ def _under(stream, device):
 
 
 def _rows(name, t):
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be [rows, columns], got {list(t.shape)}")
+    """Shape and device of a [rows, columns] CUDA tensor."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be [rows, columns], got {list(shape)}")
     if not t.is_cuda:
         raise TypeError("switch_moe tensors must be CUDA tensors")
-    return t.shape[0], t.shape[1], t.device
+    return shape, t.device
 
 
 def norm_fwd(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None, inplace: bool = False, out=None,
@@ -603,34 +625,39 @@ def norm_fwd(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None, in
     weight [d] float32; out_dtype float32, bfloat16 or float8_e4m3fn (default: residual's).  Returns a dict with
     sum (None without a delta; residual itself with ``inplace``), out, scale ([T], 8-bit outputs only) and rstd [T].
     ``out`` takes the result of an earlier call of the same sizes, which is overwritten."""
-    import torch
-    T, dm, dev = _rows("residual", residual)
+    shape, dev = _rows("residual", residual)
     if stream is not None:
         with _under(stream, dev):
             return norm_fwd(residual, weight, delta, eps, out_dtype, inplace, out)
-    out_dtype = residual.dtype if out_dtype is None else out_dtype
-    e4m3 = out_dtype == torch.float8_e4m3fn
-    halves = (torch.float32, torch.bfloat16)
-    pr = _want("residual", residual, (T, dm), halves, dev)
-    pd = _want("delta", delta, (T, dm), halves, dev)
-    pw = _want("weight", weight, (dm,), (torch.float32,), dev)
+    z = _names or _torch_names()
+    T, dm = shape
+    dtype = residual.dtype
+    if out_dtype is None:
+        out_dtype = dtype
+    out_code = _code(out_dtype)
+    pr, pd = _want("residual", residual, shape, z.floats, dev), _want("delta", delta, shape, z.floats, dev)
+    pw = _want("weight", weight, (dm,), z.f32, dev)
     stored = delta is not None and not inplace
-
-    def make():
-        return dict(sum=torch.empty_like(residual) if stored else None,
-                    out=torch.empty(T, dm, dtype=out_dtype, device=dev),
-                    scale=torch.empty(T, dtype=torch.float32, device=dev) if e4m3 else None,
-                    rstd=torch.empty(T, dtype=torch.float32, device=dev))
-
-    out = _result(out, ("norm_fwd", T, dm, residual.dtype, out_dtype, stored, dev), make)
-    if delta is not None and inplace:
-        out["sum"] = residual
-    d = SwitchNormDims(T, dm, dtype_code(residual.dtype), SWITCH_F32 if delta is None else dtype_code(delta.dtype),
-                       _code(out_dtype), eps)
-    total, scale = out["sum"], out["scale"]
-    _launch(lib().switch_norm_fwd, "switch_norm_fwd", dev, ctypes.byref(d), pr, pd, pw,
-            None if total is None else total.data_ptr(), out["out"].data_ptr(),
-            None if scale is None else scale.data_ptr(), out["rstd"].data_ptr())
+    key = ("norm_fwd", shape, dtype, out_dtype, stored, dev)
+    if out is None or type(out) is not _Result or out.key != key:
+        empty, f32 = z.torch.empty, z.torch.float32
+        out = _result(out, key, lambda: dict(
+            sum=z.torch.empty_like(residual) if stored else None, out=empty(shape, dtype=out_dtype, device=dev),
+            scale=empty(T, dtype=f32, device=dev) if out_dtype == z.e4m3 else None,
+            rstd=empty(T, dtype=f32, device=dev)))
+    own = out.own
+    out.update(own)
+    total, scale, codes = own["sum"], own["scale"], z.codes
+    if total is not None:
+        ps = total.data_ptr()
+    elif delta is not None:
+        out["sum"], ps = residual, pr
+    else:
+        ps = None
+    d = SwitchNormDims(T, dm, codes[dtype], SWITCH_F32 if delta is None else codes[delta.dtype],
+                       out_code, eps)
+    _launch(lib().switch_norm_fwd, "switch_norm_fwd", dev, ctypes.byref(d), pr, pd, pw, ps, own["out"].data_ptr(),
+            None if scale is None else scale.data_ptr(), own["rstd"].data_ptr())
     return out
 
 
@@ -638,47 +665,50 @@ def norm_bwd(sum, weight, rstd, dout, dsum=None, out=None, stream=None):
     """Gradient of norm_fwd (switch_norm_bwd): from dout [T, d] float32 (the gradient of its out) and dsum [T, d]
     float32 (the gradient of its sum from elsewhere, or None), dresidual [T, d] (of residual and of delta alike) and
     dweight [d], float32.  sum is norm_fwd's sum, or residual where there was no delta."""
-    import torch
-    T, dm, dev = _rows("sum", sum)
+    shape, dev = _rows("sum", sum)
     if stream is not None:
         with _under(stream, dev):
             return norm_bwd(sum, weight, rstd, dout, dsum, out)
-    f32 = (torch.float32,)
-    ps = _want("sum", sum, (T, dm), (torch.float32, torch.bfloat16), dev)
-    pw, pr = _want("weight", weight, (dm,), f32, dev), _want("rstd", rstd, (T,), f32, dev)
-    pg, pu = _want("dout", dout, (T, dm), f32, dev), _want("dsum", dsum, (T, dm), f32, dev)
-    out = _result(out, ("norm_bwd", T, dm, dev), lambda: dict(
-        dresidual=torch.empty(T, dm, dtype=torch.float32, device=dev),
-        dweight=torch.empty(dm, dtype=torch.float32, device=dev)))
-    d = SwitchNormDims(T, dm, dtype_code(sum.dtype), SWITCH_F32, SWITCH_F32, 0.0)
+    z = _names or _torch_names()
+    T, dm = shape
+    f32 = z.f32
+    ps, pw = _want("sum", sum, shape, z.floats, dev), _want("weight", weight, (dm,), f32, dev)
+    pr, pg, pu = (_want("rstd", rstd, (T,), f32, dev), _want("dout", dout, shape, f32, dev),
+                  _want("dsum", dsum, shape, f32, dev))
+    empty = z.torch.empty
+    out = _result(out, ("norm_bwd", shape, dev), lambda: dict(
+        dresidual=empty(shape, dtype=f32[0], device=dev), dweight=empty(dm, dtype=f32[0], device=dev)))
+    own = out.own
+    d = SwitchNormDims(T, dm, z.codes[sum.dtype], SWITCH_F32, SWITCH_F32, 0.0)
     size = switch_norm_workspace_size(d)
-    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    ws = empty(size, dtype=z.torch.uint8, device=dev)
     _launch(lib().switch_norm_bwd, "switch_norm_bwd", dev, ctypes.byref(d), ps, pw, pr, pg, pu,
-            out["dresidual"].data_ptr(), out["dweight"].data_ptr(), ws.data_ptr(), size)
+            own["dresidual"].data_ptr(), own["dweight"].data_ptr(), ws.data_ptr(), size)
     return out
 
 
 def quantize_rows(x, out=None, stream=None):
     """x [..., cols] float32 or bfloat16 in 8 bits (switch_quantize_rows): a dict with q (float8_e4m3fn, x's shape)
     and scale (float32, x's shape without the last dimension); x is about q * scale."""
-    import torch
     if not x.is_cuda:
         raise TypeError("switch_moe tensors must be CUDA tensors")
-    if x.dim() < 1:
+    shape, dev = x.shape, x.device
+    if len(shape) < 1:
         raise ValueError("x must have rows")
-    dev, cols = x.device, x.shape[-1]
     if stream is not None:
         with _under(stream, dev):
             return quantize_rows(x, out)
+    z = _names or _torch_names()
     rows = 1
-    for n in x.shape[:-1]:
+    for n in shape[:-1]:
         rows *= n
-    px = _want("x", x, x.shape, (torch.float32, torch.bfloat16), dev)
-    out = _result(out, ("quantize_rows", x.shape, dev), lambda: dict(
-        q=torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev),
-        scale=torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)))
-    _launch(lib().switch_quantize_rows, "switch_quantize_rows", dev, rows, cols, dtype_code(x.dtype), px,
-            out["q"].data_ptr(), out["scale"].data_ptr())
+    px = _want("x", x, shape, z.floats, dev)
+    empty = z.torch.empty
+    out = _result(out, ("quantize_rows", shape, dev), lambda: dict(
+        q=empty(shape, dtype=z.e4m3, device=dev), scale=empty(shape[:-1], dtype=z.torch.float32, device=dev)))
+    own = out.own
+    _launch(lib().switch_quantize_rows, "switch_quantize_rows", dev, rows, shape[-1], z.codes[x.dtype], px,
+            own["q"].data_ptr(), own["scale"].data_ptr())
     return out
 
 
@@ -712,11 +742,12 @@ class FewLayer:
         self.w_in_scale, self.w_out_scale = w_in_scale, w_out_scale
         self.top_k, self.capacity, self.capacity_factor, self.flags = int(top_k), capacity, capacity_factor, int(flags)
         self.num_experts, self.d_ff, self.d_model, self.device, self.dtype = N, F, dm, dev, w_in.dtype
-        self._sizes = {}
+        self._x_types = {False: (torch.bfloat16,) if e4m3 else (w_in.dtype,), True: (torch.float8_e4m3fn,)}
+        self._sizes = {}  # at most 65 entries: more tokens are refused
         self._dims(1)  # refuses sizes that no call could run with
 
     def _dims(self, T):
-        """(dims, workspace bytes) of calls with T tokens."""
+        """(dims, their address, workspace bytes) of calls with T tokens."""
         got = self._sizes.get(T)
         if got is None:
             if self.capacity is not None:
@@ -726,49 +757,50 @@ class FewLayer:
             else:
                 C = max(1, T)
             d = dims(T, self.d_model, self.d_ff, self.num_experts, C, _code(self.dtype), self.flags)
-            got = self._sizes[T] = (d, switch_few_workspace_size(d, self.top_k))
+            got = self._sizes[T] = (d, ctypes.byref(d), switch_few_workspace_size(d, self.top_k))
         return got
 
     def __call__(self, x, x_scale=None, out=None, ws=None, stream=None):
         """x [T, d] of the experts' type (8-bit experts: bfloat16, or float8_e4m3fn with x_scale [T] float32).
         Returns a dict with y [T, d] float32 (no residual), aux, expert / gate / slot ([T], or [T, 2] with top_k 2)
         and counts.  ``out`` takes the result of an earlier call with as many tokens, which is overwritten."""
-        import torch
         dev = self.device
         if stream is not None:
             with _under(stream, dev):
                 return self(x, x_scale, out, ws)
-        if x.dim() != 2:
-            raise ValueError(f"x must be [T, {self.d_model}], got {list(x.shape)}")
-        T, k = x.shape[0], self.top_k
-        if self.dtype != torch.float8_e4m3fn:
-            if x_scale is not None:
-                raise ValueError("x_scale goes with float8_e4m3fn experts and x")
-            types = (self.dtype,)
-        else:
-            types = (torch.bfloat16,) if x_scale is None else (torch.float8_e4m3fn,)
-        px = _want("x", x, (T, self.d_model), types, dev)
-        pxs = _want("x_scale", x_scale, (T,), (torch.float32,), dev)
-        d, size = self._dims(T)
+        z = _names or _torch_names()
+        shape, k = x.shape, self.top_k
+        if len(shape) != 2:
+            raise ValueError(f"x must be [T, {self.d_model}], got {list(shape)}")
+        T = shape[0]
+        if x_scale is not None and self.w_in_scale is None:
+            raise ValueError("x_scale goes with float8_e4m3fn experts and x")
+        px = _want("x", x, (T, self.d_model), self._x_types[x_scale is not None], dev)
+        pxs = _want("x_scale", x_scale, (T,), z.f32, dev)
+        got = self._sizes.get(T)
+        d, ref, size = self._dims(T) if got is None else got
+        empty = z.torch.empty
 
         def make():
-            shape = (T,) if k == 1 else (T, k)
-            return dict(y=torch.empty(T, self.d_model, dtype=torch.float32, device=dev),
-                        expert=torch.empty(shape, dtype=torch.int32, device=dev),
-                        gate=torch.empty(shape, dtype=torch.float32, device=dev),
-                        slot=torch.empty(shape, dtype=torch.int32, device=dev),
-                        counts=torch.empty(self.num_experts, dtype=torch.int32, device=dev),
-                        aux=torch.empty(1, dtype=torch.float32, device=dev))
+            pairs, f32, i32 = (T,) if k == 1 else (T, k), z.torch.float32, z.torch.int32
+            return dict(y=empty(T, self.d_model, dtype=f32, device=dev), expert=empty(pairs, dtype=i32, device=dev),
+                        gate=empty(pairs, dtype=f32, device=dev), slot=empty(pairs, dtype=i32, device=dev),
+                        counts=empty(self.num_experts, dtype=i32, device=dev), aux=empty(1, dtype=f32, device=dev))
 
         out = _result(out, ("few", T, k, self.d_model, self.num_experts, dev), make)
+        own = out.own
         if ws is None:
-            ws = torch.empty(size, dtype=torch.uint8, device=dev)
+            ws = empty(size, dtype=z.torch.uint8, device=dev)
+        else:
+            size = ws.numel() * ws.element_size()
+            if ws.device != dev:
+                raise ValueError(f"ws must be on {dev}, got {ws.device}")
         bias, si, so = self.logit_bias, self.w_in_scale, self.w_out_scale
-        _launch(lib().switch_layer_fwd_few, "switch_layer_fwd_few", dev, ctypes.byref(d), k, px, pxs,
+        _launch(lib().switch_layer_fwd_few, "switch_layer_fwd_few", dev, ref, k, px, pxs,
                 self.w_r.data_ptr(), None if bias is None else bias.data_ptr(), self.w_in.data_ptr(),
                 None if si is None else si.data_ptr(), self.w_out.data_ptr(), None if so is None else so.data_ptr(),
-                out["y"].data_ptr(), out["expert"].data_ptr(), out["gate"].data_ptr(), out["slot"].data_ptr(),
-                out["counts"].data_ptr(), out["aux"].data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+                own["y"].data_ptr(), own["expert"].data_ptr(), own["gate"].data_ptr(), own["slot"].data_ptr(),
+                own["counts"].data_ptr(), own["aux"].data_ptr(), _ptr(ws), size)
         out["capacity"], out["flags"], out["workspace"] = d.capacity, d.flags, ws
         return out
 

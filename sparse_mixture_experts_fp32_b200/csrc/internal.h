@@ -171,7 +171,7 @@ cudaError_t launch_ffn_tc_bwd_dw(const switch_dims_t &dims, const void *a, const
                                  int rows, int nout, float *out, DeviceStatus *st, cudaStream_t stream);
 
 // Residual + norm, its gradient, rows in 8 bits.
-constexpr int kNormBwdBlocks = 296;  // blocks of the gradient kernel at most (two per SM): rows of its partial sums
+constexpr int kNormBwdSms = 148;  // SMs of a B200, for the number of the gradient kernel's blocks (host only)
 size_t norm_workspace_bytes(const switch_norm_dims_t &n);
 cudaError_t launch_norm_fwd(const switch_norm_dims_t &n, const void *residual, const void *delta, const float *weight,
                             void *sum, void *out, float *scale, float *rstd, cudaStream_t stream);

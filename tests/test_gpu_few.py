@@ -267,7 +267,7 @@ def test_handle_results_and_stale_workspaces():
     p = make(5, 128, 256, 4, "bf16", seed=13)
     layer = sm.FewLayer(p["w_r"], p["w_in"], p["w_out"], top_k=2)
     want = layer(p["x"])
-    d, size = layer._dims(5)
+    size = layer._dims(5)[2]
     ws = torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda")  # needs no initialisation
     r = layer(p["x"], ws=ws)
     assert torch.equal(r["y"], want["y"]) and r["workspace"] is ws

@@ -76,7 +76,7 @@ def test_few_workspace(L):
         got = sm.switch_few_workspace_size(d, k)
         pairs = T * k
         assert got >= pairs * (1024 + 4096) * 4 + T * 8 * 4
-        assert got <= (1 << 16) + max(2 * pairs, 256) * (1024 + 4096 + 8) * 4 + T * 8 * 4
+        assert got <= (1 << 16) + 512 * (1024 + 4096 + 8) * 4 + T * 8 * 4
     assert L.switch_few_workspace_size(ctypes.byref(fdims()), 1, None) == NULL
 
 
