@@ -171,108 +171,139 @@ cudaError_t router_typed(const FewArgs &p, int zero_ints, int want_xmax, cudaStr
 constexpr int kSimtThreads = 256;
 constexpr int kSimtBlocks = 2;  // per SM
 constexpr int kSimtWarps = kSimtThreads / 32;
-constexpr int kSimtRows = 8;    // weight rows of an item
-constexpr int kSimtTokens = 8;  // tokens of a group
+constexpr int kSimtRows = 8;  // weight rows of an item
 
+template <int TOK>
 struct SimtShared {
     FewPlan plan;
-    float red[kSimtWarps][kSimtRows * kSimtTokens];
-    int item, go, last;
+    float red[kSimtWarps][kSimtRows * TOK];
+    int item, last;
 };
 
-// part[r][j] = sum_k w[r][k] in[j][k] over this warp's share of k, for
-// kSimtRows rows of weights and m tokens, reduced over the warp's lanes.
-template <typename W, typename X, int V>
-__device__ __forceinline__ void simt_dots(const W *w, int64_t rows_left, int K, const X *const *in, int m, int warp,
-                                          int lane, float *red) {
-    float acc[kSimtRows][kSimtTokens];
+// v[0..7] of every lane summed over the warp: lane l (a multiple of 4) is left
+// with the sum of v[l / 4].  Each exchange halves the values, so eight sums
+// take 9 shuffles and not 40.
+__device__ __forceinline__ float sum8(float (&v)[8], int lane) {
+    float u[4], w[2];
+    const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4;
 #pragma unroll
-    for (int r = 0; r < kSimtRows; ++r)
+    for (int i = 0; i < 4; ++i) {
+        const float away = h16 ? v[i] : v[4 + i], mine = h16 ? v[4 + i] : v[i];
+        u[i] = mine + __shfl_xor_sync(0xffffffffu, away, 16);
+    }
 #pragma unroll
-        for (int j = 0; j < kSimtTokens; ++j) acc[r][j] = 0.f;
-    const W *wr[kSimtRows];
+    for (int i = 0; i < 2; ++i) {
+        const float away = h8 ? u[i] : u[2 + i], mine = h8 ? u[2 + i] : u[i];
+        w[i] = mine + __shfl_xor_sync(0xffffffffu, away, 8);
+    }
+    float s = (h4 ? w[1] : w[0]) + __shfl_xor_sync(0xffffffffu, h4 ? w[0] : w[1], 4);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    return s + __shfl_xor_sync(0xffffffffu, s, 1);
+}
+
+// red[j * 8 + r] = sum_k w[r][k] x_j[k], x_j the row token[j] (or j) of `in`,
+// over this warp's share of k (every eighth step of 32 V elements), for
+// kSimtRows rows of weights and m <= TOK tokens; rows past `rows_left` repeat
+// the last one.  U steps' weights are in flight together, as many as the
+// registers beside the accumulators hold.
+template <typename W, typename X, int V, int TOK>
+__device__ __forceinline__ void simt_dots(const W *w, int rows_left, int K, const X *in, const int *token, int m,
+                                          int pitch, int warp, int lane, float *red) {
+    float acc[TOK][kSimtRows];
 #pragma unroll
-    for (int r = 0; r < kSimtRows; ++r) wr[r] = w + (r < rows_left ? r : rows_left - 1) * (int64_t)K;
-    for (int k = (warp * 32 + lane) * V; k < K; k += kSimtThreads * V) {
-        float wv[kSimtRows][V];
+    for (int j = 0; j < TOK; ++j)
 #pragma unroll
-        for (int r = 0; r < kSimtRows; ++r) load_elems<W, V>(wr[r] + k, wv[r]);
+        for (int r = 0; r < kSimtRows; ++r) acc[j][r] = 0.f;
+    constexpr int kStride = kSimtThreads * V, U = TOK == 4 ? (V == 1 ? 6 : 2) : (V == 1 ? 4 : 1);
+    for (int k0 = (warp * 32 + lane) * V; k0 < K; k0 += U * kStride) {
+        float wv[U][kSimtRows][V];
 #pragma unroll
-        for (int j = 0; j < kSimtTokens; ++j) {
-            if (j < m) {
-                float xv[V];
-                load_elems<X, V>(in[j] + k, xv);
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < V; ++i)
+            for (int r = 0; r < kSimtRows; ++r) {
+                const int k = k0 + u * kStride;
+                if (u == 0 || k < K) {
+                    load_elems<W, V>(w + (uint32_t)(min(r, rows_left - 1) * K + k), wv[u][r]);
+                } else {
 #pragma unroll
-                    for (int r = 0; r < kSimtRows; ++r) acc[r][j] = fmaf(wv[r][i], xv[i], acc[r][j]);
+                    for (int i = 0; i < V; ++i) wv[u][r][i] = 0.f;
+                }
+            }
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) {
+            if (j >= m) break;
+            const X *x = in + (int64_t)(token != nullptr ? token[j] : j) * pitch;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + u * kStride;
+                if (u == 0 || k < K) {
+                    float xv[V];
+                    load_elems<X, V>(x + k, xv);
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+#pragma unroll
+                        for (int r = 0; r < kSimtRows; ++r) acc[j][r] = fmaf(wv[u][r][i], xv[i], acc[j][r]);
+                }
             }
         }
     }
 #pragma unroll
-    for (int j = 0; j < kSimtTokens; ++j) {
-        if (j < m) {
-#pragma unroll
-            for (int r = 0; r < kSimtRows; ++r) {
-                float a = acc[r][j];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-                if (lane == 0) red[r * kSimtTokens + j] = a;
-            }
-        }
+    for (int j = 0; j < TOK; ++j) {
+        if (j >= m) break;
+        const float s = sum8(acc[j], lane);
+        if ((lane & 3) == 0) red[j * kSimtRows + (lane >> 2)] = s;
     }
 }
 
-template <typename W, typename X, int V>
+// A block takes an item: 8 weight rows of one expert, their length dealt out
+// to its 8 warps, for up to TOK tokens.  (Warps that take items of their own,
+// without the barriers, measured slower: their x rows come eight times as often.)
+// V: elements that a lane takes of a weight row at a time.
+template <typename W, typename X, int V, int TOK>
 __global__ void __launch_bounds__(kSimtThreads, kSimtBlocks) few_experts_simt_kernel(const FewArgs p) {
-    __shared__ SimtShared s;
+    __shared__ SimtShared<TOK> s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();  // the logits and the zeroed counters
     int next = 0;
     if (tid == 0) next = atomicAdd(&p.ctr->claim, 1);
-    few_plan(p, s.plan, kSimtTokens, kSimtThreads);
+    few_plan(p, s.plan, TOK, kSimtThreads);
     if (tid < 128) few_gates(p, s.plan, tid, blockIdx.x == 0);
     const int tiles_h = (p.F + kSimtRows - 1) / kSimtRows, tiles_o = (p.d + kSimtRows - 1) / kSimtRows;
     const int groups = s.plan.groups, items_h = groups * tiles_h, items = items_h + groups * tiles_o;
     for (;;) {
         if (tid == 0) {
-            s.item = next;
-            s.go = 1;
-            if (next < items) {
-                const int mine = next;
+            int mine = next;
+            if (mine < items) {
                 next = atomicAdd(&p.ctr->claim, 1);  // the following item's claim runs while this one is computed
-                if (mine >= items_h)
-                    s.go = wait_counter_geq(&p.ctr->done[(mine - items_h) % groups], tiles_h, p.status, 71);
+                if (mine >= items_h &&
+                    !wait_counter_geq(&p.ctr->done[(mine - items_h) % groups], tiles_h, p.status, 71))
+                    mine = items;
             }
+            s.item = mine;
         }
         __syncthreads();
         const int item = s.item;
-        if (item >= items || !s.go) break;
+        if (item >= items) break;
         const bool second = item >= items_h;
-        const int g = second ? (item - items_h) % groups : item / tiles_h;
-        const int tile = second ? (item - items_h) / groups : item % tiles_h;
+        const int r0 = second ? item - items_h : item, q0 = r0 / (second ? groups : tiles_h);
+        const int rest = r0 - q0 * (second ? groups : tiles_h);
+        const int g = second ? rest : q0, tile = second ? q0 : rest;
         const int e = s.plan.g_expert[g], a0 = s.plan.g_first[g], m = s.plan.g_size[g];
         const int row0 = tile * kSimtRows, rows = second ? p.d : p.F, K = second ? p.F : p.d;
         const W *w = static_cast<const W *>(second ? p.w_out : p.w_in) + ((int64_t)e * rows + row0) * K;
-        if (second) {
-            const float *in[kSimtTokens];
-#pragma unroll
-            for (int j = 0; j < kSimtTokens; ++j) in[j] = p.h + (int64_t)(a0 + min(j, m - 1)) * p.F;
-            simt_dots<W, float, V>(w, rows - row0, K, in, m, warp, lane, s.red[warp]);
-        } else {
-            const X *in[kSimtTokens];
-#pragma unroll
-            for (int j = 0; j < kSimtTokens; ++j)
-                in[j] = static_cast<const X *>(p.x) + (int64_t)s.plan.token[a0 + min(j, m - 1)] * p.d;
-            simt_dots<W, X, V>(w, rows - row0, K, in, m, warp, lane, s.red[warp]);
-        }
+        if (second)
+            simt_dots<W, float, V, TOK>(w, rows - row0, K, p.h + (int64_t)a0 * p.F, nullptr, m, p.F, warp, lane,
+                                         s.red[warp]);
+        else
+            simt_dots<W, X, V, TOK>(w, rows - row0, K, static_cast<const X *>(p.x), s.plan.token + a0, m, p.d, warp,
+                                     lane, s.red[warp]);
         __syncthreads();
-        if (tid < kSimtRows * kSimtTokens) {
-            const int j = tid / kSimtRows, r = tid % kSimtRows, row = row0 + r;
-            if (j < m && row < rows) {
+        if (tid < kSimtRows * m) {
+            const int j = tid / kSimtRows, row = row0 + tid % kSimtRows;
+            if (row < rows) {
                 float v = 0.f;
 #pragma unroll
-                for (int q = 0; q < kSimtWarps; ++q) v += s.red[q][r * kSimtTokens + j];
+                for (int q = 0; q < kSimtWarps; ++q) v += s.red[q][tid];
                 if (second) {
                     if (p.w_out_scale != nullptr) v *= p.w_out_scale[(int64_t)e * p.d + row];
                     p.o[(int64_t)(a0 + j) * p.d + row] = v;
@@ -293,23 +324,27 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtBlocks) few_experts_simt_ke
             if (s.last) {  // y of the tile's rows for every token
                 for (int i = tid; i < p.T * kSimtRows; i += kSimtThreads) {
                     const int t = i / kSimtRows, row = row0 + i % kSimtRows;
+                    if (row >= p.d) continue;
                     float y = 0.f;
                     for (int c = 0; c < p.k; ++c) {
                         const int a = s.plan.pos[t * p.k + c];
-                        if (a >= 0 && row < p.d) y += s.plan.gate[t * p.k + c] * __ldcg(p.o + (int64_t)a * p.d + row);
+                        if (a >= 0) y += s.plan.gate[t * p.k + c] * __ldcg(p.o + (int64_t)a * p.d + row);
                     }
-                    if (row < p.d) p.y[(int64_t)t * p.d + row] = y;
+                    p.y[(int64_t)t * p.d + row] = y;
                 }
             }
         }
-        __syncthreads();
     }
 }
 
 template <typename W, typename X, int V>
 cudaError_t experts_simt(const FewArgs &p, cudaStream_t stream) {
-    return launch_kernel(few_experts_simt_kernel<W, X, V>, dim3(device_sm_count() * kSimtBlocks), dim3(kSimtThreads), 0,
-                         stream, true, p);
+    // Few pairs: groups of up to 4 tokens, whose accumulators leave registers for more weights in flight (2 tokens
+    // of 4096 x 10000: 113 us, with 8 117 us); many: 8, so that weights are read for more tokens at a time (32
+    // tokens top-2 of 1024 x 2048: 106 us, with 4 121 us).
+    const bool few = p.T * p.k <= 16;
+    return launch_kernel(few ? few_experts_simt_kernel<W, X, V, 4> : few_experts_simt_kernel<W, X, V, 8>,
+                         dim3(device_sm_count() * kSimtBlocks), dim3(kSimtThreads), 0, stream, true, p);
 }
 
 }  // namespace
@@ -397,9 +432,9 @@ cudaError_t launch_few_router(const FewArgs &p, int x_dtype, int zero_ints, bool
 cudaError_t launch_few_experts_simt(const FewArgs &p, int w_dtype, int x_dtype, cudaStream_t stream) {
     launch_begin(K_FEW_EXPERTS_SIMT, stream);
     cudaError_t err;
-    if (w_dtype == SWITCH_BF16) err = experts_simt<__nv_bfloat16, __nv_bfloat16, 8>(p, stream);
-    else if (w_dtype == SWITCH_E4M3 && x_dtype == SWITCH_E4M3) err = experts_simt<uint8_t, uint8_t, 8>(p, stream);
-    else if (w_dtype == SWITCH_E4M3) err = experts_simt<uint8_t, __nv_bfloat16, 8>(p, stream);
+    if (w_dtype == SWITCH_BF16) err = experts_simt<__nv_bfloat16, __nv_bfloat16, 4>(p, stream);
+    else if (w_dtype == SWITCH_E4M3 && x_dtype == SWITCH_E4M3) err = experts_simt<uint8_t, uint8_t, 4>(p, stream);
+    else if (w_dtype == SWITCH_E4M3) err = experts_simt<uint8_t, __nv_bfloat16, 4>(p, stream);
     else if (p.d % 4 == 0 && p.F % 4 == 0) err = experts_simt<float, float, 4>(p, stream);
     else err = experts_simt<float, float, 1>(p, stream);
     launch_end(stream);
