@@ -172,27 +172,35 @@ __device__ __forceinline__ int scale_exponent(uint32_t bits) {
 __device__ __forceinline__ float pow2(int k) { return __int_as_float((127 + min(127, k)) << 23); }  // k >= -126
 __device__ __forceinline__ float unscale(int k) { return k == 1000 ? __int_as_float(0x7fc00000) : pow2(-k); }
 
-// 16 values -> TERMS rows of 16 e4m3 bytes: term i holds what the terms before
-// it left, times 16^i.
+// 16 values of at most 256 -> TERMS rows of 16 e4m3 bytes, term i holding what
+// the terms before it left, times 16^i.  The terms are cut in float16, two
+// values at a time: its 11 bits hold what three terms do exactly (the third is
+// what the first two leave of them), and what it leaves of v, times 16^3, makes
+// the fourth and fifth (2 terms: v is a bfloat16, which float16 holds exactly).
 template <int TERMS>
-__device__ __forceinline__ void store_e4m3_terms(uint8_t *tile, int row0, int chunk, float (&v)[16]) {
+__device__ __forceinline__ void store_e4m3_terms(uint8_t *tile, int row0, int chunk, const float (&v)[16]) {
+    static_assert(TERMS == 2 || TERMS == 5, "x, h");
+    uint32_t w[TERMS][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        __half2 left = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+        const float2 top = __half22float2(left);
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) {
+            if (t == 3)
+                left = __floats2half2_rn((v[2 * i] - top.x) * 4096.f, (v[2 * i + 1] - top.y) * 4096.f);
+            const __nv_fp8x2_storage_t q = __nv_cvt_halfraw2_to_fp8x2((__half2_raw)left, __NV_SATFINITE, __NV_E4M3);
+            if (i & 1) w[t][i >> 1] |= (uint32_t)q << 16;
+            else w[t][i >> 1] = q;
+            if (t + 1 < TERMS && t != 2)
+                left = __hmul2(__hsub2(left, __half2(__nv_cvt_fp8x2_to_halfraw2(q, __NV_E4M3))), __float2half2_rn(16.f));
+        }
+    }
 #pragma unroll
     for (int t = 0; t < TERMS; ++t) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const __nv_fp8x2_storage_t q =
-                __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-            if (i & 1) w[i >> 1] |= (uint32_t)q << 16;
-            else w[i >> 1] = q;
-            if (t + 1 < TERMS) {
-                const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(q, __NV_E4M3)));
-                v[2 * i] = (v[2 * i] - f.x) * 16.f;
-                v[2 * i + 1] = (v[2 * i + 1] - f.y) * 16.f;
-            }
-        }
         const int row = row0 + t;
-        *reinterpret_cast<uint4 *>(tile + row * 128 + ((chunk ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(tile + row * 128 + ((chunk ^ (row & 7)) << 4)) =
+            make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
     }
 }
 
@@ -457,7 +465,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 s.queue[q] = item < w.items ? item : -1;
                 mbar_arrive(&s.q_full[q]);
                 if (item >= w.items) break;
-                claimed = atomicAdd(&p.ctr->claim, 1);  // the next item's claim runs while this one's loads are issued
+                // The next item's claim runs while this one's loads are issued.  Where the second product has an
+                // item per block at most, a block takes one: a second, claimed ahead by a block that waits, would
+                // come after it while other blocks have none.
+                const bool last = item >= w.items_h && w.items - w.items_h <= (int)gridDim.x;
+                claimed = last ? w.items : atomicAdd(&p.ctr->claim, 1);
                 const Item it = locate(w, item);
                 const int e = s.plan.g_expert[it.g];
                 for (int kc = it.k0; kc < it.k1; ++kc) {
