@@ -23,6 +23,7 @@ High level (allocate outputs and workspace with torch):
 from __future__ import annotations
 
 import ctypes
+import functools
 from pathlib import Path
 
 _PKG = Path(__file__).resolve().parent
@@ -661,6 +662,12 @@ def norm_fwd(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None, in
     return out
 
 
+@functools.lru_cache(maxsize=64)
+def _norm_bwd_dims(T, d_model, code):
+    d = SwitchNormDims(T, d_model, code, SWITCH_F32, SWITCH_F32, 0.0)
+    return d, ctypes.byref(d), switch_norm_workspace_size(d)
+
+
 def norm_bwd(sum, weight, rstd, dout, dsum=None, out=None, stream=None):
     """Gradient of norm_fwd (switch_norm_bwd): from dout [T, d] float32 (the gradient of its out) and dsum [T, d]
     float32 (the gradient of its sum from elsewhere, or None), dresidual [T, d] (of residual and of delta alike) and
@@ -679,10 +686,9 @@ def norm_bwd(sum, weight, rstd, dout, dsum=None, out=None, stream=None):
     out = _result(out, ("norm_bwd", shape, dev), lambda: dict(
         dresidual=empty(shape, dtype=f32[0], device=dev), dweight=empty(dm, dtype=f32[0], device=dev)))
     own = out.own
-    d = SwitchNormDims(T, dm, z.codes[sum.dtype], SWITCH_F32, SWITCH_F32, 0.0)
-    size = switch_norm_workspace_size(d)
+    _, ref, size = _norm_bwd_dims(T, dm, z.codes[sum.dtype])
     ws = empty(size, dtype=z.torch.uint8, device=dev)
-    _launch(lib().switch_norm_bwd, "switch_norm_bwd", dev, ctypes.byref(d), ps, pw, pr, pg, pu,
+    _launch(lib().switch_norm_bwd, "switch_norm_bwd", dev, ref, ps, pw, pr, pg, pu,
             own["dresidual"].data_ptr(), own["dweight"].data_ptr(), ws.data_ptr(), size)
     return out
 

@@ -343,49 +343,49 @@ __device__ __forceinline__ void add_accumulator(uint32_t taddr, int m, float (&v
     }
 }
 
-// y of one output row for the group's tokens in `mask`, whose parts are all there.
+// y of one output row for the first B tokens of `mask` (positions from a0 on),
+// whose parts are all there; returns the mask without them.  The loads of U
+// parts of all B tokens are in flight together.
+template <int B, int U>
+__device__ __forceinline__ uint32_t combine_tokens(const FewArgs &p, const FewPlan &s, int splits, int64_t step, int a0,
+                                                   uint32_t mask, int row) {
+    int t[B];
+    float y[B];
+#pragma unroll
+    for (int u = 0; u < B; ++u) {
+        t[u] = s.token[a0 + __ffs(mask) - 1];  // past the last one: the last one again
+        y[u] = 0.f;
+        if (u == B - 1 || (mask & (mask - 1))) mask &= mask - 1;
+    }
+    for (int c = 0; c < p.k; ++c) {
+        float o[B];
+        const float *src[B];
+#pragma unroll
+        for (int u = 0; u < B; ++u) {
+            o[u] = 0.f;
+            src[u] = p.o + (int64_t)max(s.pos[t[u] * p.k + c], 0) * p.d + row;
+        }
+#pragma unroll U
+        for (int q = 0; q < splits; ++q)
+#pragma unroll
+            for (int u = 0; u < B; ++u) o[u] += __ldcg(src[u] + q * step);
+#pragma unroll
+        for (int u = 0; u < B; ++u)
+            if (s.pos[t[u] * p.k + c] >= 0) y[u] += s.gate[t[u] * p.k + c] * o[u];
+    }
+#pragma unroll
+    for (int u = 0; u < B; ++u) p.y[(int64_t)t[u] * p.d + row] = y[u];
+    return mask;
+}
+
 __device__ __forceinline__ void combine_row(const FewArgs &p, const FewPlan &s, int splits, int A, int a0,
                                             uint32_t mask, int row) {
     const int64_t step = (int64_t)A * p.d;
-    if ((mask & (mask - 1)) == 0) {  // one token, its parts in flight together
-        const int t = s.token[a0 + __ffs(mask) - 1];
-        float y = 0.f;
-        for (int c = 0; c < p.k; ++c) {
-            const int a = s.pos[t * p.k + c];
-            if (a < 0) continue;
-            const float *src = p.o + (int64_t)a * p.d + row;
-            float o = 0.f;
-#pragma unroll 4
-            for (int q = 0; q < splits; ++q) o += __ldcg(src + q * step);
-            y += s.gate[t * p.k + c] * o;
-        }
-        p.y[(int64_t)t * p.d + row] = y;
-        return;
-    }
-    while (mask) {  // four tokens at a time, their loads in flight together
-        int t[4];
-        float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            t[u] = s.token[a0 + __ffs(mask) - 1];  // past the last one: the last one again
-            if (mask & (mask - 1)) mask &= mask - 1;
-            else if (u == 3) mask = 0;
-        }
-        for (int c = 0; c < p.k; ++c) {
-            float o[4] = {0.f, 0.f, 0.f, 0.f};
-            const float *src[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) src[u] = p.o + (int64_t)max(s.pos[t[u] * p.k + c], 0) * p.d + row;
-#pragma unroll 4
-            for (int q = 0; q < splits; ++q)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) o[u] += __ldcg(src[u] + q * step);
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (s.pos[t[u] * p.k + c] >= 0) y[u] += s.gate[t[u] * p.k + c] * o[u];
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) p.y[(int64_t)t[u] * p.d + row] = y[u];
+    while (mask) {
+        const int n = __popc(mask);
+        mask = n == 1 ? combine_tokens<1, 8>(p, s, splits, step, a0, mask, row)
+               : n <= 4 ? combine_tokens<4, 8>(p, s, splits, step, a0, mask, row)
+                        : combine_tokens<8, 4>(p, s, splits, step, a0, mask, row);
     }
 }
 

@@ -14,7 +14,8 @@
 // there and written once.  A group of `tpr` threads holds a row, 8 elements (16
 // or 32 bytes) per thread; widths that are no multiple of 8 take the same
 // kernels with one element per thread and step, since their rows start at any
-// alignment.  Blocks live for one row group (a loop over rows that loads the
+// alignment (four steps where a block can hold the row so: 65536 x 257 to 8
+// bits 84 us, eight steps 102 us).  Blocks live for one row group (a loop over rows that loads the
 // next one early measured 20 % slower: 237 us); only the gradient, which keeps
 // column sums, loops.  Sums and the norm are float32 (8 terms per thread, then
 // a tree); the maxima are taken on the bit patterns of |v|, whose order is that
@@ -427,13 +428,14 @@ template <typename R, typename D, typename O>
 void norm_fwd_typed(const switch_norm_dims_t &n, const void *residual, const void *delta, const float *weight,
                     void *sum, void *out, float *scale, float *rstd, cudaStream_t stream) {
     const bool wide = n.d_model % 8 == 0;
-    const RowShape s = wide ? shape_of(n.d_model / 8, 1) : shape_of(n.d_model, 8);
+    const RowShape s = wide ? shape_of(n.d_model / 8, 1) : shape_of(n.d_model, n.d_model <= 4096 ? 4 : 8);
     const dim3 grid((unsigned)((n.T + s.rows - 1) / s.rows)), block(s.tpr, s.rows);
 #define SWITCH_NORM_FWD(V, I)                                                                                  \
     norm_fwd_kernel<R, D, O, V, I><<<grid, block, 0, stream>>>(                                                \
         static_cast<const R *>(residual), static_cast<const D *>(delta), weight, static_cast<R *>(sum),        \
         static_cast<O *>(out), scale, rstd, n.T, n.d_model, n.eps)
     if (wide) SWITCH_NORM_FWD(8, 1);
+    else if (s.iters == 4) SWITCH_NORM_FWD(1, 4);
     else SWITCH_NORM_FWD(1, 8);
 #undef SWITCH_NORM_FWD
 }
@@ -479,7 +481,7 @@ void quantize_typed(int64_t rows, int cols, const void *x, void *q, float *scale
     // Four steps per thread, a row to a warp, once there are rows enough to fill the GPU with warps: 16384 x 1024
     // takes 15 us so and 19 us with one step, 4096 x 1024 6.2 us and 5.8 us.
     const bool wide = cols % 8 == 0, large = rows * (int64_t)cols > (1 << 23) || cols > 8192;
-    const RowShape s = wide ? shape_of(cols / 8, large ? 4 : 1) : shape_of(cols, cols > 8192 ? 32 : 8);
+    const RowShape s = wide ? shape_of(cols / 8, large ? 4 : 1) : shape_of(cols, cols <= 4096 ? 4 : cols <= 8192 ? 8 : 32);
     const dim3 grid((unsigned)((rows + s.rows - 1) / s.rows)), block(s.tpr, s.rows);
 #define SWITCH_QUANT(V, I, N)                                                                      \
     quantize_rows_kernel<R, V, I, N><<<grid, block, 0, stream>>>(static_cast<const R *>(x),        \
@@ -487,6 +489,7 @@ void quantize_typed(int64_t rows, int cols, const void *x, void *q, float *scale
     if (wide && s.iters == 1) SWITCH_QUANT(8, 1, 1024);
     else if (wide && s.tpr <= 256) SWITCH_QUANT(8, 4, 256);
     else if (wide) SWITCH_QUANT(8, 4, 1024);
+    else if (s.iters == 4) SWITCH_QUANT(1, 4, 1024);
     else if (s.iters == 8) SWITCH_QUANT(1, 8, 1024);
     else SWITCH_QUANT(1, 32, 1024);
 #undef SWITCH_QUANT
