@@ -12,14 +12,14 @@
 //
 // All of them are bound by memory: a row is read once into registers, reduced
 // there and written once.  A group of `tpr` threads holds a row, 8 elements (16
-// or 32 bytes) per thread; widths that are no multiple of 8 take the same
-// kernels with one element per thread and step, since their rows start at any
-// alignment (four steps where a block can hold the row so: 65536 x 257 to 8
-// bits 84 us, eight steps 102 us).  Blocks live for one row group (a loop over rows that loads the
-// next one early measured 20 % slower: 237 us); only the gradient, which keeps
-// column sums, loops.  Sums and the norm are float32 (8 terms per thread, then
-// a tree); the maxima are taken on the bit patterns of |v|, whose order is that
-// of the values and puts NaN on top, so that a row with a NaN gets a NaN scale.
+// or 32 bytes) per thread.  The eights are those of the whole tensor, which
+// start on 16 bytes whatever the width is; where the width is no multiple of 8
+// (ODD) a row's first and last eight are read and written one by one.  Blocks
+// live for one row group (a loop over rows that loads the next one early
+// measured 20 % slower: 237 us); only the gradient, which keeps column sums,
+// loops.  Sums and the norm are float32 (8 terms per thread, then a tree); the
+// maxima are taken on the bit patterns of |v|, whose order is that of the values
+// and puts NaN on top, so that a row with a NaN gets a NaN scale.
 //
 // Measured on a B200 (copy bandwidth 6549 GB/s): 131072 x 1024 bfloat16 +
 // float32 -> bfloat16 194 us (6.9 TB/s), its gradient 304 us (6.2 TB/s);
@@ -41,10 +41,15 @@ constexpr float kE4m3Max = 448.f;
 #endif
 struct None {};  // no delta
 
-template <typename T, int VEC>
-__device__ __forceinline__ void load_row(const T *p, float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        v[0] = Elem<T>::load(p, 0);
+// Eight elements of a row of d, from element j on.  ODD: j may be up to 7
+// before the row, and the eight may reach past its end; what is not of the row
+// is neither read (0 instead) nor written.  `ones`: every eight one by one.
+template <typename T, bool ODD>
+__device__ __forceinline__ void load8(const T *row, int j, int d, bool ones, float (&v)[8]) {
+    const T *p = row + j;
+    if (ODD && (ones || j < 0 || j + 8 > d)) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = j + k >= 0 && j + k < d ? Elem<T>::load(p, k) : 0.f;
     } else if constexpr (sizeof(T) == 4) {
         const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
@@ -59,10 +64,24 @@ __device__ __forceinline__ void load_row(const T *p, float (&v)[VEC]) {
     }
 }
 
-template <typename T, int VEC>
-__device__ __forceinline__ void store_row(T *p, const float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        Elem<T>::store(p, 0, v[0]);
+// The same of a vector that starts on 16 bytes, whatever j is: ODD reads it one by one (it stays in L1).
+template <bool ODD>
+__device__ __forceinline__ void load_weight(const float *w, int j, int d, float (&v)[8]) {
+    if constexpr (ODD) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = j + k >= 0 && j + k < d ? __ldg(w + j + k) : 0.f;
+    } else {
+        load8<float, false>(w, j, d, false, v);
+    }
+}
+
+template <typename T, bool ODD>
+__device__ __forceinline__ void store8(T *row, int j, int d, bool ones, const float (&v)[8]) {
+    T *p = row + j;
+    if (ODD && (ones || j < 0 || j + 8 > d)) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (j + k >= 0 && j + k < d) Elem<T>::store(p, k, v[k]);
     } else if constexpr (sizeof(T) == 4) {
         reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
         reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -72,21 +91,38 @@ __device__ __forceinline__ void store_row(T *p, const float (&v)[VEC]) {
     }
 }
 
-template <int VEC>
-__device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        *p = (uint8_t)__nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
-    } else {
-        uint32_t w[2];
+template <bool ODD>
+__device__ __forceinline__ void store8_e4m3(uint8_t *row, int j, int d, bool ones, const float (&v)[8]) {
+    uint32_t w[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i], v[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi =
-                __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2], v[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
-            w[i] = lo | (hi << 16);
-        }
-        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i], v[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi =
+            __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2], v[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
+        w[i] = lo | (hi << 16);
     }
+    if (ODD && (ones || j < 0 || j + 8 > d)) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (j + k >= 0 && j + k < d) row[j + k] = (uint8_t)(w[k / 4] >> (8 * (k % 4)));
+    } else {
+        *reinterpret_cast<uint2 *>(row + j) = make_uint2(w[0], w[1]);
+    }
+}
+
+// First element of step i of this thread in row t: eights of the whole tensor,
+// so that they start on 16 bytes (8 in 8 bits) in every row.
+template <bool ODD>
+__device__ __forceinline__ int first_of(int i, int64_t t, int d, bool ones) {
+    return (i * (int)blockDim.x + (int)threadIdx.x) * 8 - (ODD && !ones ? (int)((t * d) & 7) : 0);
+}
+
+// Whether a block's threads, at 1024 of them, are too few for a row's eights
+// and hold the row from its own beginning instead (the last widths below 8192
+// and, in four steps, below 32768).
+template <bool ODD>
+__device__ __forceinline__ bool by_ones(int steps, int d) {
+    return ODD && (int)blockDim.x * steps * 8 < d + 7;
 }
 
 // Sum (or maximum of unsigned) over the `tpr` threads of a row; every thread
@@ -139,43 +175,24 @@ struct Quantizer {
         inv = __frcp_rn(s);
         tiny = s < 1e-30f;
     }
-    template <int VEC>
-    __device__ __forceinline__ void store(uint8_t *q, const float (&v)[VEC]) const {
-        float u[VEC];
+    template <bool ODD>
+    __device__ __forceinline__ void store(uint8_t *q, int j, int d, bool ones, const float (&v)[8]) const {
+        float u[8];
         Doubt doubt;
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
+        for (int k = 0; k < 8; ++k) {
             u[k] = v[k] * inv;
             doubt.see(u[k]);
         }
         if (tiny || doubt.any()) {
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) u[k] = s == 0.f ? 0.f : __fdiv_rn(v[k], s);  // a row of zeros: scale 0
+            for (int k = 0; k < 8; ++k) u[k] = s == 0.f ? 0.f : __fdiv_rn(v[k], s);  // a row of zeros: scale 0
         }
-        store_e4m3<VEC>(q, u);
+        store8_e4m3<ODD>(q, j, d, ones, u);
     }
 };
 
-// The row in registers -> e4m3 and its scale.
-template <int VEC, int ITERS>
-__device__ __forceinline__ void quantize_row(const float (&v)[ITERS][VEC], int d, int tpr, float *part, bool live,
-                                             uint8_t *q, float *scale) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < ITERS; ++i)
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) top = max(top, __float_as_uint(v[i][k]) & 0x7fffffffu);
-    const Quantizer z(row_max(top, tpr, part));
-    if (!live) return;
-    if (threadIdx.x == 0) *scale = z.s;
-#pragma unroll
-    for (int i = 0; i < ITERS; ++i) {
-        const int j = (i * tpr + (int)threadIdx.x) * VEC;
-        if (j < d) z.store<VEC>(q + j, v[i]);
-    }
-}
-
-template <typename R, typename D, typename O, int VEC, int ITERS>
+template <typename R, typename D, typename O, bool ODD>
 __global__ void __launch_bounds__(1024)
     norm_fwd_kernel(const R *residual, const D *delta, const float *__restrict__ weight, R *sum, O *out,
                     float *__restrict__ scale, float *__restrict__ rstd, int64_t T, int d, float eps) {
@@ -185,64 +202,51 @@ __global__ void __launch_bounds__(1024)
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = t < T;
     const int64_t row = live ? t * d : 0;
-    float s[ITERS][VEC];
+    const bool ones = by_ones<ODD>(1, d);
+    const int j = first_of<ODD>(0, t, d, ones);
+    const bool mine = live && j < d;
+    float s[8];
     float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < ITERS; ++i) {
-        const int j = (i * tpr + (int)threadIdx.x) * VEC;
+    for (int k = 0; k < 8; ++k) s[k] = 0.f;
+    if (mine) {
+        load8<R, ODD>(residual + row, j, d, ones, s);
+        if constexpr (kDelta) {
+            float a[8];
+            load8<D, ODD>(delta + row, j, d, ones, a);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) s[i][k] = 0.f;
-        if (live && j < d) {
-            load_row<R, VEC>(residual + row + j, s[i]);
-            if constexpr (kDelta) {
-                float a[VEC];
-                load_row<D, VEC>(delta + row + j, a);
-#pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    s[i][k] += a[k];
-                    // the sum is normalised as it is stored: the backward pass reads the stored one
-                    if constexpr (sizeof(R) == 2) s[i][k] = bf16_bits_to_float(float_to_bf16_bits(s[i][k]));
-                }
+            for (int k = 0; k < 8; ++k) {
+                s[k] += a[k];
+                // the sum is normalised as it is stored: the backward pass reads the stored one
+                if constexpr (sizeof(R) == 2) s[k] = bf16_bits_to_float(float_to_bf16_bits(s[k]));
             }
-        }
-    }
-    if constexpr (kDelta) {
-        if (sum != nullptr) {
-#pragma unroll
-            for (int i = 0; i < ITERS; ++i) {
-                const int j = (i * tpr + (int)threadIdx.x) * VEC;
-                if (live && j < d) store_row<R, VEC>(sum + row + j, s[i]);
-            }
+            if (sum != nullptr) store8<R, ODD>(sum + row, j, d, ones, s);
         }
     }
 #pragma unroll
-    for (int i = 0; i < ITERS; ++i)
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) ss = fmaf(s[i][k], s[i][k], ss);
+    for (int k = 0; k < 8; ++k) ss = fmaf(s[k], s[k], ss);
     const float r = __frcp_rn(__fsqrt_rn(row_sum(ss, tpr, part[0]) / (float)d + eps));
     if (live && threadIdx.x == 0 && rstd != nullptr) rstd[t] = r;
+    if (j < d) {
+        float w[8];
+        load_weight<ODD>(weight, j, d, w);
 #pragma unroll
-    for (int i = 0; i < ITERS; ++i) {
-        const int j = (i * tpr + (int)threadIdx.x) * VEC;
-        if (j >= d) break;
-        float w[VEC];
-        load_row<float, VEC>(weight + j, w);
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) s[i][k] = s[i][k] * r * w[k];
+        for (int k = 0; k < 8; ++k) s[k] = s[k] * r * w[k];
     }
     if constexpr (sizeof(O) == 1) {
-        quantize_row<VEC, ITERS>(s, d, tpr, part[1], live, reinterpret_cast<uint8_t *>(out) + row, scale + t);
-    } else {
+        uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < ITERS; ++i) {
-            const int j = (i * tpr + (int)threadIdx.x) * VEC;
-            if (live && j < d) store_row<O, VEC>(out + row + j, s[i]);
-        }
+        for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(s[k]) & 0x7fffffffu);
+        const Quantizer z(row_max(top, tpr, part[1]));
+        if (live && threadIdx.x == 0) scale[t] = z.s;
+        if (mine) z.store<ODD>(reinterpret_cast<uint8_t *>(out) + row, j, d, ones, s);
+    } else {
+        if (mine) store8<O, ODD>(out + row, j, d, ones, s);
     }
 }
 
-template <typename R, int VEC, int ITERS, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 && VEC == 8 && sizeof(R) == 2 ? 6 : 1)
+template <typename R, int ITERS, int THREADS, bool ODD>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 && sizeof(R) == 2 && !ODD ? 6 : 1)
     quantize_rows_kernel(const R *__restrict__ x, uint8_t *__restrict__ q, float *__restrict__ scale, int64_t rows,
                          int cols) {
     __shared__ float part[32];
@@ -250,13 +254,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && VEC == 8 && sizeof(
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = t < rows;
     const int64_t row = live ? t * cols : 0;
-    if constexpr (VEC == 8 && sizeof(R) == 2) {
+    if constexpr (!ODD && sizeof(R) == 2) {
         // the row stays in its 16 bits until it is rounded: half the registers, twice the rows in flight
         uint4 raw[ITERS];
         uint32_t top2 = 0;
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
-            const int j = (i * tpr + (int)threadIdx.x) * VEC;
+            const int j = first_of<false>(i, t, cols, false);
             raw[i] = live && j < cols ? *reinterpret_cast<const uint4 *>(x + row + j) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
@@ -269,25 +273,38 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && VEC == 8 && sizeof(
         if (threadIdx.x == 0) scale[t] = z.s;
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
-            const int j = (i * tpr + (int)threadIdx.x) * VEC;
+            const int j = first_of<false>(i, t, cols, false);
             if (j >= cols) break;
             const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
             float v[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 v[2 * k] = __uint_as_float(w[k] << 16), v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-            z.store<8>(q + row + j, v);
+            z.store<false>(q + row, j, cols, false, v);
         }
     } else {
-        float v[ITERS][VEC];
+        const bool ones = by_ones<ODD>(ITERS, cols);
+        float v[ITERS][8];
+        uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
-            const int j = (i * tpr + (int)threadIdx.x) * VEC;
+            const int j = first_of<ODD>(i, t, cols, ones);
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) v[i][k] = 0.f;
-            if (live && j < cols) load_row<R, VEC>(x + row + j, v[i]);
+            for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+            if (live && j < cols) load8<R, ODD>(x + row, j, cols, ones, v[i]);
         }
-        quantize_row<VEC, ITERS>(v, cols, tpr, part, live, q + row, scale + t);
+#pragma unroll
+        for (int i = 0; i < ITERS; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[i][k]) & 0x7fffffffu);
+        const Quantizer z(row_max(top, tpr, part));
+        if (!live) return;
+        if (threadIdx.x == 0) scale[t] = z.s;
+#pragma unroll
+        for (int i = 0; i < ITERS; ++i) {
+            const int j = first_of<ODD>(i, t, cols, ones);
+            if (j < cols) z.store<ODD>(q + row, j, cols, ones, v[i]);
+        }
     }
 }
 
@@ -296,97 +313,75 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && VEC == 8 && sizeof(
 // over its rows in part_dw[block]; dweight_kernel adds the blocks in order.
 // A thread holds 8 elements of a row, so that enough blocks fit on an SM to
 // keep memory busy (32 elements: 600 us at 131072 x 1024, 8: 304 us), and loads
-// the next row's while this one's sum is formed.
-template <typename R, int VEC, int ITERS, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? (VEC == 8 ? 4 : 2) : 1)
+// the next row's while this one's sum is formed.  Its columns are the same in
+// all its rows: ODD takes a number of blocks that makes them 8 rows apart.
+template <typename R, int THREADS, bool ODD>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? (ODD ? 3 : 4) : 1)
     norm_bwd_kernel(const R *__restrict__ sum, const float *__restrict__ weight, const float *__restrict__ rstd,
                     const float *dout, const float *dsum, float *dres, float *__restrict__ part_dw, int64_t T, int d) {
     extern __shared__ float columns[];  // [blockDim.y][d] when a block holds several rows
     __shared__ float part[2][32];
     const int tpr = blockDim.x;
-    float w[ITERS][VEC], dw[ITERS][VEC];
+    const int64_t t_first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const bool ones = by_ones<ODD>(1, d);
+    const int j = first_of<ODD>(0, t_first, d, ones);
+    float w[8], dw[8];
 #pragma unroll
-    for (int i = 0; i < ITERS; ++i) {
-        const int j = (i * tpr + (int)threadIdx.x) * VEC;
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) w[i][k] = dw[i][k] = 0.f;
-        if (j < d) load_row<float, VEC>(weight + j, w[i]);
-    }
+    for (int k = 0; k < 8; ++k) w[k] = dw[k] = 0.f;
+    if (j < d) load_weight<ODD>(weight, j, d, w);
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    float h[ITERS][VEC], g[ITERS][VEC];
+    float h[8], g[8];
     float r = 0.f;
     auto load = [&](int64_t t) {
         const bool live = t < T;
         r = live ? rstd[t] : 0.f;
 #pragma unroll
-        for (int i = 0; i < ITERS; ++i) {
-            const int j = (i * tpr + (int)threadIdx.x) * VEC;
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) h[i][k] = g[i][k] = 0.f;
-            if (live && j < d) {
-                load_row<R, VEC>(sum + t * d + j, h[i]);
-                load_row<float, VEC>(dout + t * d + j, g[i]);
-            }
+        for (int k = 0; k < 8; ++k) h[k] = g[k] = 0.f;
+        if (live && j < d) {
+            load8<R, ODD>(sum + t * d, j, d, ones, h);
+            load8<float, ODD>(dout + t * d, j, d, ones, g);
         }
     };
-    load((int64_t)blockIdx.x * blockDim.y + threadIdx.y);
+    load(t_first);
     int turn = 0;
     for (int64_t t0 = (int64_t)blockIdx.x * blockDim.y; t0 < T; t0 += step) {
         const int64_t t = t0 + threadIdx.y;
-        const bool live = t < T;
+        const bool mine = t < T && j < d;
         const float rt = r;
-        float u[ITERS][VEC], b[ITERS][VEC];
+        float u[8], b[8];
         float dot = 0.f;
 #pragma unroll
-        for (int i = 0; i < ITERS; ++i) {
-            const int j = (i * tpr + (int)threadIdx.x) * VEC;
+        for (int k = 0; k < 8; ++k) u[k] = 0.f;
+        if (mine && dsum != nullptr) load8<float, ODD>(dsum + t * d, j, d, ones, u);
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) u[i][k] = 0.f;
-            if (live && j < d && dsum != nullptr) load_row<float, VEC>(dsum + t * d + j, u[i]);
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                const float hat = h[i][k] * rt;
-                dw[i][k] = fmaf(g[i][k], hat, dw[i][k]);
-                const float gw = g[i][k] * w[i][k];
-                dot = fmaf(gw, hat, dot);
-                u[i][k] = fmaf(rt, gw, u[i][k]);
-                b[i][k] = rt * hat;
-            }
+        for (int k = 0; k < 8; ++k) {
+            const float hat = h[k] * rt;
+            dw[k] = fmaf(g[k], hat, dw[k]);
+            const float gw = g[k] * w[k];
+            dot = fmaf(gw, hat, dot);
+            u[k] = fmaf(rt, gw, u[k]);
+            b[k] = rt * hat;
         }
         load(t + step);
         const float m = row_sum(dot, tpr, part[turn]) / (float)d;
         turn ^= 1;
+        if (mine) {
 #pragma unroll
-        for (int i = 0; i < ITERS; ++i) {
-            const int j = (i * tpr + (int)threadIdx.x) * VEC;
-            if (live && j < d) {
-#pragma unroll
-                for (int k = 0; k < VEC; ++k) u[i][k] = fmaf(-m, b[i][k], u[i][k]);
-                store_row<float, VEC>(dres + t * d + j, u[i]);
-            }
+            for (int k = 0; k < 8; ++k) u[k] = fmaf(-m, b[k], u[k]);
+            store8<float, ODD>(dres + t * d, j, d, ones, u);
         }
     }
-    float *mine = part_dw + (int64_t)blockIdx.x * d;
-    if (blockDim.y == 1) {
+    float *to = blockDim.y == 1 ? part_dw + (int64_t)blockIdx.x * d : columns + threadIdx.y * d;
 #pragma unroll
-        for (int i = 0; i < ITERS; ++i) {
-            const int j = (i * tpr + (int)threadIdx.x) * VEC;
-            if (j < d) store_row<float, VEC>(mine + j, dw[i]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < ITERS; ++i) {
-            const int j = (i * tpr + (int)threadIdx.x) * VEC;
-#pragma unroll
-            for (int k = 0; k < VEC; ++k)
-                if (j + k < d) columns[threadIdx.y * d + j + k] = dw[i][k];
-        }
+    for (int k = 0; k < 8; ++k)
+        if (j + k >= 0 && j + k < d) to[j + k] = dw[k];
+    if (blockDim.y > 1) {
         __syncthreads();
         const int threads = blockDim.x * blockDim.y;
-        for (int j = threadIdx.y * tpr + threadIdx.x; j < d; j += threads) {
+        for (int c = threadIdx.y * tpr + threadIdx.x; c < d; c += threads) {
             float a = 0.f;
-            for (int y = 0; y < (int)blockDim.y; ++y) a += columns[y * d + j];
-            mine[j] = a;
+            for (int y = 0; y < (int)blockDim.y; ++y) a += columns[y * d + c];
+            part_dw[(int64_t)blockIdx.x * d + c] = a;
         }
     }
     pdl_launch_dependents();
@@ -420,24 +415,22 @@ struct RowShape {
     int tpr, rows, iters;
 };
 RowShape shape_of(int n, int iters) {
-    const int tpr = (n + 32 * iters - 1) / (32 * iters) * 32;
+    const int tpr = n > 1024 * iters ? 1024 : (n + 32 * iters - 1) / (32 * iters) * 32;
     return {tpr, tpr == 32 ? 8 : tpr >= 128 ? 1 : 128 / tpr, iters};
 }
+
+// Eights that cover a row of d elements, wherever in one it begins.
+int eights(int d) { return d % 8 == 0 ? d / 8 : (d + 7 + 7) / 8; }
 
 template <typename R, typename D, typename O>
 void norm_fwd_typed(const switch_norm_dims_t &n, const void *residual, const void *delta, const float *weight,
                     void *sum, void *out, float *scale, float *rstd, cudaStream_t stream) {
-    const bool wide = n.d_model % 8 == 0;
-    const RowShape s = wide ? shape_of(n.d_model / 8, 1) : shape_of(n.d_model, n.d_model <= 4096 ? 4 : 8);
+    const RowShape s = shape_of(eights(n.d_model), 1);
     const dim3 grid((unsigned)((n.T + s.rows - 1) / s.rows)), block(s.tpr, s.rows);
-#define SWITCH_NORM_FWD(V, I)                                                                                  \
-    norm_fwd_kernel<R, D, O, V, I><<<grid, block, 0, stream>>>(                                                \
-        static_cast<const R *>(residual), static_cast<const D *>(delta), weight, static_cast<R *>(sum),        \
-        static_cast<O *>(out), scale, rstd, n.T, n.d_model, n.eps)
-    if (wide) SWITCH_NORM_FWD(8, 1);
-    else if (s.iters == 4) SWITCH_NORM_FWD(1, 4);
-    else SWITCH_NORM_FWD(1, 8);
-#undef SWITCH_NORM_FWD
+    auto *kernel = n.d_model % 8 == 0 ? norm_fwd_kernel<R, D, O, false> : norm_fwd_kernel<R, D, O, true>;
+    kernel<<<grid, block, 0, stream>>>(static_cast<const R *>(residual), static_cast<const D *>(delta), weight,
+                                       static_cast<R *>(sum), static_cast<O *>(out), scale, rstd, n.T, n.d_model,
+                                       n.eps);
 }
 
 template <typename R, typename D>
@@ -463,48 +456,37 @@ void norm_bwd_typed(const switch_norm_dims_t &n, const RowShape &s, int blocks, 
                     cudaStream_t stream) {
     const dim3 block(s.tpr, s.rows);
     const size_t smem = s.rows > 1 ? (size_t)s.rows * n.d_model * sizeof(float) : 0;
-#define SWITCH_NORM_BWD(V, I, N)                                                                                  \
-    norm_bwd_kernel<R, V, I, N><<<blocks, block, smem, stream>>>(static_cast<const R *>(sum), weight, rstd, dout, \
-                                                                 dsum, dres, part, n.T, n.d_model)
-    if (s.tpr <= 256) {
-        if (n.d_model % 8 == 0) SWITCH_NORM_BWD(8, 1, 256);
-        else SWITCH_NORM_BWD(1, 8, 256);
-    } else {
-        if (n.d_model % 8 == 0) SWITCH_NORM_BWD(8, 1, 1024);
-        else SWITCH_NORM_BWD(1, 8, 1024);
-    }
-#undef SWITCH_NORM_BWD
+    const bool odd = n.d_model % 8 != 0;
+    auto *kernel = s.tpr <= 256 ? (odd ? norm_bwd_kernel<R, 256, true> : norm_bwd_kernel<R, 256, false>)
+                                : (odd ? norm_bwd_kernel<R, 1024, true> : norm_bwd_kernel<R, 1024, false>);
+    kernel<<<blocks, block, smem, stream>>>(static_cast<const R *>(sum), weight, rstd, dout, dsum, dres, part, n.T,
+                                            n.d_model);
 }
 
 template <typename R>
 void quantize_typed(int64_t rows, int cols, const void *x, void *q, float *scale, cudaStream_t stream) {
     // Four steps per thread, a row to a warp, once there are rows enough to fill the GPU with warps: 16384 x 1024
     // takes 15 us so and 19 us with one step, 4096 x 1024 6.2 us and 5.8 us.
-    const bool wide = cols % 8 == 0, large = rows * (int64_t)cols > (1 << 23) || cols > 8192;
-    const RowShape s = wide ? shape_of(cols / 8, large ? 4 : 1) : shape_of(cols, cols <= 4096 ? 4 : cols <= 8192 ? 8 : 32);
+    const bool large = rows * (int64_t)cols > (1 << 23) || cols > 8192, odd = cols % 8 != 0;
+    const RowShape s = shape_of(eights(cols), large ? 4 : 1);
     const dim3 grid((unsigned)((rows + s.rows - 1) / s.rows)), block(s.tpr, s.rows);
-#define SWITCH_QUANT(V, I, N)                                                                      \
-    quantize_rows_kernel<R, V, I, N><<<grid, block, 0, stream>>>(static_cast<const R *>(x),        \
-                                                                 static_cast<uint8_t *>(q), scale, rows, cols)
-    if (wide && s.iters == 1) SWITCH_QUANT(8, 1, 1024);
-    else if (wide && s.tpr <= 256) SWITCH_QUANT(8, 4, 256);
-    else if (wide) SWITCH_QUANT(8, 4, 1024);
-    else if (s.iters == 4) SWITCH_QUANT(1, 4, 1024);
-    else if (s.iters == 8) SWITCH_QUANT(1, 8, 1024);
-    else SWITCH_QUANT(1, 32, 1024);
-#undef SWITCH_QUANT
+    auto *kernel =
+        s.iters == 1 ? (odd ? quantize_rows_kernel<R, 1, 1024, true> : quantize_rows_kernel<R, 1, 1024, false>)
+        : s.tpr <= 256 ? (odd ? quantize_rows_kernel<R, 4, 256, true> : quantize_rows_kernel<R, 4, 256, false>)
+                       : (odd ? quantize_rows_kernel<R, 4, 1024, true> : quantize_rows_kernel<R, 4, 1024, false>);
+    kernel<<<grid, block, 0, stream>>>(static_cast<const R *>(x), static_cast<uint8_t *>(q), scale, rows, cols);
 }
 
-RowShape bwd_shape(const switch_norm_dims_t &n) {
-    return n.d_model % 8 == 0 ? shape_of(n.d_model / 8, 1) : shape_of(n.d_model, 8);
-}
+RowShape bwd_shape(const switch_norm_dims_t &n) { return shape_of(eights(n.d_model), 1); }
 
 int bwd_blocks(const switch_norm_dims_t &n) {
     const RowShape s = bwd_shape(n);
     const int64_t groups = (n.T + s.rows - 1) / s.rows;
-    // as many blocks as are resident: 64 registers a thread leave an SM 1024 threads (128 half as many)
-    const int64_t most = (int64_t)kNormBwdSms * (n.d_model % 8 == 0 || s.tpr > 256 ? 1024 : 512) / (s.tpr * s.rows);
-    return (int)(groups < most ? groups : most);
+    // As many blocks as are resident: 64 registers a thread leave an SM 1024 threads (80, for odd widths, 768).
+    const bool odd = n.d_model % 8 != 0;
+    const int64_t most = (int64_t)kNormBwdSms * (odd && s.tpr <= 256 ? 768 : 1024) / (s.tpr * s.rows);
+    const int64_t blocks = groups < most ? groups : most;
+    return (int)(odd ? (blocks + 7) / 8 * 8 : blocks);
 }
 
 }  // namespace

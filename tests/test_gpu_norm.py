@@ -41,7 +41,7 @@ def check_e4m3(q, scale, v, slack):
 
 
 SIZES = [(1, 1), (1, 1024), (3, 7), (5, 8), (2, 255), (9, 768), (33, 1032), (4, 4099), (1030, 40), (1500, 333),
-         (3, 8191), (2, 8192), (1100, 2056), (1027, 8192)]
+         (3, 8191), (2, 8192), (1100, 2056), (1027, 8192), (17, 8185), (600, 8189), (3000, 9), (2500, 511)]
 
 
 @pytest.mark.parametrize("T,d", SIZES)
@@ -73,7 +73,7 @@ def test_norm_fwd(T, d, res, delta, out):
         assert ((got["out"].double() - v).abs() <= v.abs() * (half + 44 * U) + 1e-40).all()
 
 
-@pytest.mark.parametrize("T,d", SIZES + [(7, 32768), (3, 32765), (1100, 12288)])
+@pytest.mark.parametrize("T,d", SIZES + [(7, 32768), (3, 32765), (1100, 12288), (300, 32767), (40, 8193), (2000, 8185)])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_quantize_rows(T, d, dtype):
     x = rows(T, d, dtype, 4, 0.1)
