@@ -339,7 +339,8 @@ switch_status_t switch_layer_bwd(const switch_dims_t *dims, const void *x, const
  * valid index.
  * Errors: SWITCH_ERR_SHAPE for T > SWITCH_FEW_MAX_TOKENS, top_k, or N < top_k;
  * SWITCH_ERR_NULL for a missing scale, SWITCH_ERR_DTYPE for a scale that the
- * type has no use for; otherwise as switch_layer_fwd.  The workspace needs no
+ * type has no use for; otherwise as switch_layer_fwd.  No output may overlap an
+ * input, another output or the workspace.  The workspace needs no
  * initialisation and serves one call at a time.  Identical inputs give
  * identical bytes. */
 #define SWITCH_FEW_MAX_TOKENS 64

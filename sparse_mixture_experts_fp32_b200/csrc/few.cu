@@ -177,7 +177,7 @@ template <int TOK>
 struct SimtShared {
     FewPlan plan;
     float red[kSimtWarps][kSimtRows * TOK];
-    int item, last;
+    int item, go, last;
 };
 
 // v[0..7] of every lane summed over the warp: lane l (a multiple of 4) is left
@@ -267,23 +267,30 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtBlocks) few_experts_simt_ke
     int next = 0;
     if (tid == 0) next = atomicAdd(&p.ctr->claim, 1);
     few_plan(p, s.plan, TOK, kSimtThreads);
-    if (tid < 128) few_gates(p, s.plan, tid, blockIdx.x == 0);
     const int tiles_h = (p.F + kSimtRows - 1) / kSimtRows, tiles_o = (p.d + kSimtRows - 1) / kSimtRows;
     const int groups = s.plan.groups, items_h = groups * tiles_h, items = items_h + groups * tiles_o;
+    bool gates = false;
     for (;;) {
         if (tid == 0) {
-            int mine = next;
-            if (mine < items) {
-                next = atomicAdd(&p.ctr->claim, 1);  // the following item's claim runs while this one is computed
-                if (mine >= items_h &&
-                    !wait_counter_geq(&p.ctr->done[(mine - items_h) % groups], tiles_h, p.status, 71))
-                    mine = items;
-            }
-            s.item = mine;
+            s.item = next;
+            if (next < items) next = atomicAdd(&p.ctr->claim, 1);  // runs while this item is computed
         }
         __syncthreads();
         const int item = s.item;
+        if (!gates && item >= items_h) {  // between the products, when the first one's last parts are under way
+            gates = true;
+            if (tid < 128)
+                few_gates(p, s.plan, tid, blockIdx.x == 0, [] {
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    return true;
+                });
+        }
         if (item >= items) break;
+        if (item >= items_h) {
+            if (tid == 0) s.go = wait_counter_geq(&p.ctr->done[(item - items_h) % groups], tiles_h, p.status, 71);
+            __syncthreads();
+            if (!s.go) break;
+        }
         const bool second = item >= items_h;
         const int r0 = second ? item - items_h : item, q0 = r0 / (second ? groups : tiles_h);
         const int rest = r0 - q0 * (second ? groups : tiles_h);

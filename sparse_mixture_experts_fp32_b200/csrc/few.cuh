@@ -183,21 +183,23 @@ __device__ inline void few_plan(const FewArgs &p, FewPlan &s, int group_max, int
     __syncthreads();
 }
 
-// The gates, by four warps (`tid` = 0..127) that share named barrier 1; with
-// `outputs` (one block) the call's routing outputs too.
+// The gates, by four warps (`tid` = 0..127) for which meet() is a barrier; with
+// `outputs` (one block) the call's routing outputs too.  meet() returns false
+// where it gave up, and so does this.
 // aux = N / T^2 sum_t sum_n f_n p_tn, f_n the first choices of expert n:
 // float64, in a fixed order.
-__device__ inline void few_gates(const FewArgs &p, FewPlan &s, int tid, bool outputs) {
+template <typename Meet>
+__device__ __forceinline__ bool few_gates(const FewArgs &p, FewPlan &s, int tid, bool outputs, Meet meet) {
     const int warp = tid >> 5, lane = tid & 31;
     double aux = 0.0;
     if (outputs) {
         for (int n = tid; n < p.N; n += 128) s.cnt[n] = s.first[n] = 0;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (!meet()) return false;
         for (int i = tid; i < p.T * p.k; i += 128) {
             atomicAdd(&s.cnt[s.expert[i]], 1);
             if (p.k == 1 || (i & 1) == 0) atomicAdd(&s.first[s.expert[i]], 1);
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (!meet()) return false;
     }
     float v[kFewMaxN / 32], next[kFewMaxN / 32];
     if (warp < p.T) few_logits(p, warp, lane, next);
@@ -239,7 +241,7 @@ __device__ inline void few_gates(const FewArgs &p, FewPlan &s, int tid, bool out
         for (int o = 16; o > 0; o >>= 1) aux += __shfl_xor_sync(0xffffffffu, aux, o);
         if (lane == 0) s.aux[warp] = aux;
     }
-    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (!meet()) return false;
     if (outputs) {
         for (int i = tid; i < p.T * p.k; i += 128)
             p.expert[i] = s.expert[i], p.gate[i] = s.gate[i], p.slot[i] = s.slot[i];
@@ -247,6 +249,7 @@ __device__ inline void few_gates(const FewArgs &p, FewPlan &s, int tid, bool out
         if (tid == 0)
             *p.aux = (float)(((s.aux[0] + s.aux[1]) + (s.aux[2] + s.aux[3])) * (double)p.N / ((double)p.T * p.T));
     }
+    return true;
 }
 
 __device__ __forceinline__ int32_t atom_add_acq_rel_gpu(int32_t *p, int32_t v) {

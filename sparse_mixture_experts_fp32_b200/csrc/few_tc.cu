@@ -61,7 +61,7 @@ struct TcShared {
     uint64_t full_a[kMaxStages], full_b[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[kMaxBufs], acc_empty[kMaxBufs];
     uint64_t q_full[kQueue], q_empty[kQueue];
-    uint64_t drain;
+    uint64_t drain, meet;
     uint32_t tmem;
     int queue[kQueue];
     int ready[kFewMaxA];  // groups whose first product is complete
@@ -150,12 +150,12 @@ __device__ __forceinline__ bool wait_ready_cta(const int *flag, DeviceStatus *st
     return true;
 }
 
-// Next item from the queue, for one warp; -1: no more, or a wait gave up.
+// Next item from the queue, for one warp; -1: no more, -2: the wait gave up.
 __device__ __forceinline__ int next_item(TcShared &s, uint32_t &n, int lane, DeviceStatus *status) {
     const int q = n % kQueue;
     const uint32_t parity = (n / kQueue) & 1u;
     ++n;
-    if (!mbar_wait(&s.q_full[q], parity, status, 81)) return -1;
+    if (!mbar_wait(&s.q_full[q], parity, status, 81)) return -2;
     const int item = s.queue[q];
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.q_empty[q]);
@@ -415,6 +415,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mbar_init(&s.q_empty[i], kConsumers);
             }
             mbar_init(&s.drain, 1);
+            mbar_init(&s.meet, 4);
             fence_barrier_init();
         }
         __syncwarp();
@@ -550,9 +551,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const bool late = w.items_h <= (int)gridDim.x;
         while (ok) {
             const int item = late || gates ? next_item(s, n, lane, p.status) : 0;
+            if (item == -2) break;
             if (!gates && (!late || item < 0 || item >= w.items_h)) {
                 gates = true;
-                few_gates(p, s.plan, tid - 64, blockIdx.x == 0);
+                // (a barrier that gives up: one of the four warps may have left after a wait of its own did)
+                uint32_t turn = 0;
+                ok = few_gates(p, s.plan, tid - 64, blockIdx.x == 0, [&] {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.meet);
+                    const bool met = mbar_wait(&s.meet, turn, p.status, 94);
+                    turn ^= 1u;
+                    return __all_sync(0xffffffffu, met);
+                });
+                if (!ok) break;
                 for (int t = blockIdx.x; t < p.T; t += gridDim.x)  // tokens that no expert keeps
                     if (s.plan.pos[t * p.k] < 0 && s.plan.pos[t * p.k + p.k - 1] < 0)
                         for (int j = tid - 64; j < p.d; j += 128) p.y[(int64_t)t * p.d + j] = 0.f;

@@ -367,6 +367,61 @@ def test_streams_and_graphs(w, x):
             assert torch.equal(a["y"], b["y"]) and torch.equal(a["slot"], b["slot"])
 
 
+def test_captured_behind_a_join_of_streams():
+    """A call whose stream has just waited for another one, eagerly and captured: its first kernel may start early
+    only behind both."""
+    p = make(9, 256, 512, 6, "bf16", seed=17)
+    layer = sm.FewLayer(p["w_r"], p["w_in"], p["w_out"], top_k=2)
+    want = layer(p["x"])
+    x, src, side = torch.zeros_like(p["x"]), p["x"].clone(), torch.cuda.Stream()
+    big = torch.zeros(1 << 26, device="cuda")
+
+    def call():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            big.add_(1)  # long enough that x is late
+            x.copy_(src)
+        main.wait_stream(side)
+        return layer(x)
+
+    torch.cuda.synchronize()
+    r = call()
+    torch.cuda.synchronize()
+    assert torch.equal(r["y"], want["y"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = call()
+    for _ in range(3):
+        x.zero_(), r["y"].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(r["y"], want["y"]) and torch.equal(r["expert"], want["expert"])
+
+
+def test_calls_on_one_stream_follow_one_another():
+    """Calls of different layers and sizes behind one another without a wait, one's y the next one's delta."""
+    ps = [make(T, 256, F, N, w, seed=40 + T) for T, F, N, w in ((7, 512, 4, "bf16"), (7, 320, 9, "f32"), (7, 64, 2, "e4m3"))]
+    nw = torch.ones(256, device="cuda")
+    res = normal(gen(41), 7, 256)
+
+    def chain(wait):
+        s, delta, ys = res, None, []
+        for q in ps:
+            b = sm.block_fwd(s, nw, q["w_r"], q["w_in"], q["w_out"], delta=delta, top_k=2, capacity=7,
+                             w_in_scale=q.get("w_in_scale"), w_out_scale=q.get("w_out_scale"))
+            s, delta = b["sum"], b["y"]
+            ys.append(delta)
+            if wait:
+                torch.cuda.synchronize()
+        return ys
+
+    want = chain(True)
+    for _ in range(10):
+        for a, b in zip(chain(False), want):
+            assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("w", ["f32", "bf16", "e4m3"])
 def test_block(w):
     """Residual, norm and layer as they are used: a step's block against the definition in 64 bits.  The norm's
