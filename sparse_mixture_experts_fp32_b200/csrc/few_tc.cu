@@ -345,47 +345,46 @@ __device__ __forceinline__ void add_accumulator(uint32_t taddr, int m, float (&v
 
 // y of one output row for the first B tokens of `mask` (positions from a0 on),
 // whose parts are all there; returns the mask without them.  The loads of U
-// parts of all B tokens are in flight together.
-template <int B, int U>
-__device__ __forceinline__ uint32_t combine_tokens(const FewArgs &p, const FewPlan &s, int splits, int64_t step, int a0,
+// parts of all choices of all B tokens are in flight together.
+template <int B, int U, int K>
+__device__ __forceinline__ uint32_t combine_tokens(const FewArgs &p, const FewPlan &s, int splits, int step, int a0,
                                                    uint32_t mask, int row) {
-    int t[B];
-    float y[B];
+    int t[B], at[B][K];  // (512 rows of 8192 values at most: 32-bit offsets)
+    float o[B][K];
+    const float *src = p.o + row;
 #pragma unroll
     for (int u = 0; u < B; ++u) {
         t[u] = s.token[a0 + __ffs(mask) - 1];  // past the last one: the last one again
-        y[u] = 0.f;
         if (u == B - 1 || (mask & (mask - 1))) mask &= mask - 1;
+#pragma unroll
+        for (int c = 0; c < K; ++c) at[u][c] = max(s.pos[t[u] * K + c], 0) * p.d, o[u][c] = 0.f;
     }
-    for (int c = 0; c < p.k; ++c) {
-        float o[B];
-        const float *src[B];
-#pragma unroll
-        for (int u = 0; u < B; ++u) {
-            o[u] = 0.f;
-            src[u] = p.o + (int64_t)max(s.pos[t[u] * p.k + c], 0) * p.d + row;
-        }
 #pragma unroll U
-        for (int q = 0; q < splits; ++q)
-#pragma unroll
-            for (int u = 0; u < B; ++u) o[u] += __ldcg(src[u] + q * step);
+    for (int q = 0; q < splits; ++q)
 #pragma unroll
         for (int u = 0; u < B; ++u)
-            if (s.pos[t[u] * p.k + c] >= 0) y[u] += s.gate[t[u] * p.k + c] * o[u];
-    }
 #pragma unroll
-    for (int u = 0; u < B; ++u) p.y[(int64_t)t[u] * p.d + row] = y[u];
+            for (int c = 0; c < K; ++c) o[u][c] += __ldcg(src + at[u][c] + q * step);
+#pragma unroll
+    for (int u = 0; u < B; ++u) {
+        float y = 0.f;
+#pragma unroll
+        for (int c = 0; c < K; ++c)
+            if (s.pos[t[u] * K + c] >= 0) y += s.gate[t[u] * K + c] * o[u][c];
+        p.y[(int64_t)t[u] * p.d + row] = y;
+    }
     return mask;
 }
 
+template <int K>
 __device__ __forceinline__ void combine_row(const FewArgs &p, const FewPlan &s, int splits, int A, int a0,
                                             uint32_t mask, int row) {
-    const int64_t step = (int64_t)A * p.d;
+    const int step = A * p.d;
     while (mask) {
         const int n = __popc(mask);
-        mask = n == 1 ? combine_tokens<1, 8>(p, s, splits, step, a0, mask, row)
-               : n <= 4 ? combine_tokens<4, 8>(p, s, splits, step, a0, mask, row)
-                        : combine_tokens<8, 4>(p, s, splits, step, a0, mask, row);
+        mask = n == 1 ? combine_tokens<1, 8, K>(p, s, splits, step, a0, mask, row)
+               : n <= 4 ? combine_tokens<4, 8 / K, K>(p, s, splits, step, a0, mask, row)
+                        : combine_tokens<8, 4 / K, K>(p, s, splits, step, a0, mask, row);
     }
 }
 
@@ -641,7 +640,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                            kept * w.splits_o - 1;
                 }
                 const uint32_t mask = __ballot_sync(0xffffffffu, last);
-                if (mask && live) combine_row(p, s.plan, w.splits_o, A, a0, mask, row);
+                if (mask && live) {
+                    if (p.k == 1) combine_row<1>(p, s.plan, w.splits_o, A, a0, mask, row);
+                    else combine_row<2>(p, s.plan, w.splits_o, A, a0, mask, row);
+                }
                 __syncwarp();
             }
         }
