@@ -23,8 +23,8 @@
 //
 // Measured on a B200 (copy bandwidth 6549 GB/s): 131072 x 1024 bfloat16 +
 // float32 -> bfloat16 194 us (6.9 TB/s), its gradient 304 us (6.2 TB/s);
-// 8192 x 768 float32 + float32 -> 8 bits 16.5 us (5.0 TB/s); 131072 x 1024
-// bfloat16 to 8 bits 87 us (4.6 TB/s).
+// 8192 x 768 float32 + float32 -> 8 bits 16.1 us (5.1 TB/s); 131072 x 1024
+// bfloat16 to 8 bits 81 us (5.0 TB/s).
 #include <cuda_fp8.h>
 
 #include <type_traits>
@@ -152,21 +152,13 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, int tpr, float *part) {
     return s;
 }
 
-// e4m3's rounding of v / s is that of t = v * (1 / s), which is within 2 units in the last place of the
-// quotient, unless t is as close to the middle between two e4m3 values: in the normal range those have
-// the 20 low bits 0x80000.  Such t, and the few below the normal range, are divided for.  (A division for
-// every element bounds the kernel: 131072 x 1024 bfloat16 took 116 us with it, 90 us with this.)
-struct Doubt {
-    uint32_t middle = 0xffffffffu, small = 0xffffffffu;  // least distances (as unsigned numbers) over a thread's values
-    __device__ __forceinline__ void see(float t) {
-        const uint32_t b = __float_as_uint(t);
-        middle = min(middle, (b & 0xfffffu) - 0x7fff8u);
-        small = min(small, (b << 1) - 1u);  // a zero is not small
-    }
-    __device__ __forceinline__ bool any() const { return middle <= 0x10u || small < 0x78ffffffu; }  // |t| < 2^-6
-};
-
-// Scale of a row whose largest |v| has the bits `top`, and the rounding of its values.
+// Scale of a row whose largest |v| has the bits `top`, and the rounding of its
+// values.  e4m3's rounding of v / s is that of t = v * (1 / s), which is within
+// 2 units in the last place of the quotient, unless t is as close to the middle
+// between two e4m3 values: in the normal range those have the 20 low bits
+// 0x80000.  Eights with such a t, or with one below the normal range (2^-6), are
+// divided.  (These kernels are bound by instructions: 131072 x 1024 bfloat16
+// took 116 us with a division for every element, 81 us so.)
 struct Quantizer {
     float s, inv;
     bool tiny;  // 1 / s may overflow
@@ -175,16 +167,19 @@ struct Quantizer {
         inv = __frcp_rn(s);
         tiny = s < 1e-30f;
     }
-    template <bool ODD>
-    __device__ __forceinline__ void store(uint8_t *q, int j, int d, bool ones, const float (&v)[8]) const {
-        float u[8];
-        Doubt doubt;
+    __device__ __forceinline__ bool below_normal(float least) const { return least * inv < 0.0157f; }
+    // `divide`: an element may be below the normal range.  SEEK: look for one (a zero counts).
+    template <bool ODD, bool SEEK>
+    __device__ __forceinline__ void store(uint8_t *q, int j, int d, bool ones, const float (&v)[8], bool divide) const {
+        float u[8], least = 1.f;
+        uint32_t middle = 0xffffffffu;  // least distance from 8 below a middle
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             u[k] = v[k] * inv;
-            doubt.see(u[k]);
+            middle = __viaddmin_u32(__float_as_uint(u[k]) & 0xfffffu, 0u - 0x7fff8u, middle);
+            if (SEEK) least = fminf(least, ODD && u[k] == 0.f ? 1.f : fabsf(u[k]));  // (ODD: zeros beside the row)
         }
-        if (tiny || doubt.any()) {
+        if (tiny || divide || middle <= 0x10u || (SEEK && least < 0.015625f)) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) u[k] = s == 0.f ? 0.f : __fdiv_rn(v[k], s);  // a row of zeros: scale 0
         }
@@ -239,7 +234,7 @@ __global__ void __launch_bounds__(1024)
         for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(s[k]) & 0x7fffffffu);
         const Quantizer z(row_max(top, tpr, part[1]));
         if (live && threadIdx.x == 0) scale[t] = z.s;
-        if (mine) z.store<ODD>(reinterpret_cast<uint8_t *>(out) + row, j, d, ones, s);
+        if (mine) z.store<ODD, true>(reinterpret_cast<uint8_t *>(out) + row, j, d, ones, s, false);
     } else {
         if (mine) store8<O, ODD>(out + row, j, d, ones, s);
     }
@@ -257,7 +252,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && sizeof(R) == 2 && !
     if constexpr (!ODD && sizeof(R) == 2) {
         // the row stays in its 16 bits until it is rounded: half the registers, twice the rows in flight
         uint4 raw[ITERS];
-        uint32_t top2 = 0;
+        uint32_t top2 = 0, low2 = 0xffffffffu;  // of |x|, two at a time; low2 is one less, so that zeros do not count
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
             const int j = first_of<false>(i, t, cols, false);
@@ -265,12 +260,19 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && sizeof(R) == 2 && !
         }
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
-            top2 = __vmaxu2(top2, __vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu));
-            top2 = __vmaxu2(top2, __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu));
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t a = w[k] & 0x7fff7fffu;
+                top2 = __vmaxu2(top2, a);
+                low2 = __viaddmin_u16x2(a, 0xffffffffu, low2);
+            }
         }
         const Quantizer z(row_max(max(top2 << 16, top2 & 0xffff0000u), tpr, part));
         if (!live) return;
         if (threadIdx.x == 0) scale[t] = z.s;
+        const uint32_t low = min(low2 & 0xffffu, low2 >> 16);
+        const bool small = low < 0x7f80u && z.below_normal(bf16_bits_to_float((uint16_t)(low + 1)));
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
             const int j = first_of<false>(i, t, cols, false);
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && sizeof(R) == 2 && !
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 v[2 * k] = __uint_as_float(w[k] << 16), v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-            z.store<false>(q + row, j, cols, false, v);
+            z.store<false, false>(q + row, j, cols, false, v, small);
         }
     } else {
         const bool ones = by_ones<ODD>(ITERS, cols);
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && sizeof(R) == 2 && !
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
             const int j = first_of<ODD>(i, t, cols, ones);
-            if (j < cols) z.store<ODD>(q + row, j, cols, ones, v[i]);
+            if (j < cols) z.store<ODD, true>(q + row, j, cols, ones, v[i], false);
         }
     }
 }

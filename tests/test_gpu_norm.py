@@ -84,6 +84,30 @@ def test_quantize_rows(T, d, dtype):
     assert torch.equal(got["q"].view(torch.uint8), want.view(torch.uint8))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols,rows_", [(256, 64), (257, 64), (1024, 16384)])
+def test_quantize_rounds_the_quotient_at_middles_small_values_and_zeros(dtype, cols, rows_):
+    """Values half way between two e4m3 numbers (and next to it, in float32), below e4m3's normal range, zeros among
+    them, at scales of 2^-40 to 2^40: bit for bit the rounding of the divided value."""
+    g = torch.Generator(device="cuda").manual_seed(90)
+    code = torch.randint(0, 0x7e, (rows_, cols), device="cuda", generator=g, dtype=torch.int32).to(torch.uint8)
+    lo, hi = code.view(E4M3).float(), (code + 1).view(E4M3).float()
+    x = (lo + hi) / 2  # at most 5 significant bits: exact in bfloat16
+    if dtype == F32:
+        bits = x.view(torch.int32) + torch.randint(-3, 4, x.shape, device="cuda", generator=g, dtype=torch.int32)
+        x = torch.where(x > 0, bits.view(F32), x)
+    x = x * torch.where(torch.rand(x.shape, device="cuda", generator=g) < 0.5, -1.0, 1.0)
+    x = torch.where(torch.rand(x.shape, device="cuda", generator=g) < 0.3, torch.zeros_like(x), x)
+    x[:, 0] = 448
+    x = (x * 2.0 ** torch.randint(-40, 41, (rows_, 1), device="cuda", generator=g)).to(dtype)
+    x[1::4, 0] *= 0.9375  # a scale that is no power of two
+    got = sm.quantize_rows(x)
+    scale = (x.double().abs().amax(1) / 448).float()  # one rounding of the quotient
+    assert torch.equal(got["scale"], scale)
+    want = torch.div(x.float(), scale[:, None]).clamp(-448, 448).to(E4M3)
+    assert torch.equal(got["q"].view(torch.uint8), want.view(torch.uint8))
+
+
 def test_quantize_keeps_leading_dimensions():
     x = rows(24, 64, BF16, 5).view(2, 3, 4, 64)
     got = sm.quantize_rows(x)
