@@ -24,7 +24,7 @@
 //                 a ring of 16 KB stages
 //   warp 1        issues the MMAs
 //   warps 2-5     epilogue: 32 weight rows each
-//   warps 6-11    build the column operand of every sixth stage: gather x rows,
+//   warps 6-11    build the column operands, a stage each: gather x rows,
 //                 or add the partial sums of h, apply ReLU and cut into terms
 // The ring runs on across items and from the first product into the second:
 // weights of the second product are on their way while the first is finished.
@@ -46,6 +46,7 @@ constexpr int kRing = 215 * 1024;  // of the 227 KB a block may have: the plan a
 constexpr int kMaxBufs = 8;
 constexpr int kChain = 4;         // stages per accumulator
 constexpr int kBuilders = 6;      // 4: 3 % slower (32 tokens), 8: 4 % slower (they leave 128 registers a thread)
+constexpr int kFull = 60;         // arrivals of a built stage: 60 / w from each of its w <= 6 warps
 constexpr int kTcThreads = 32 * (6 + kBuilders);
 constexpr int kQueue = 4;
 constexpr int kConsumers = 1 + 4 + kBuilders;  // warps that read the item queue
@@ -80,6 +81,10 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
 // Instruction descriptor for kind::f8f6f4 with e4m3 A and B and an fp32 accumulator.
 __device__ __forceinline__ uint32_t idesc_e4m3_f32(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
@@ -209,15 +214,16 @@ __device__ __forceinline__ void add4(float *v, const float *p) {
     v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
 }
 
-// The column operand of stage `kc` of a first product: x rows.
+// The column operand of stage `kc` of a first product, x rows: part `part` of
+// `team`.
 template <bool E4M3, bool X8>
 __device__ __forceinline__ void build_x(const FewArgs &p, const FewPlan &s, uint8_t *tile, int a0, int m, int kc,
-                                        int my_exp, int lane) {
+                                        int my_exp, int lane, int part, int team) {
     const int tasks = m * 8;
     if constexpr (!E4M3 || X8) {  // 16 bytes per task as they are
         const uint8_t *x = static_cast<const uint8_t *>(p.x);
         const int64_t row_bytes = (int64_t)p.d * (E4M3 ? 1 : 2);
-        for (int i0 = lane; i0 < tasks; i0 += 128) {
+        for (int i0 = lane + part * 128; i0 < tasks; i0 += team * 128) {
             uint4 v[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -235,7 +241,7 @@ __device__ __forceinline__ void build_x(const FewArgs &p, const FewPlan &s, uint
         }
     } else {
         const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(p.x);
-        for (int i0 = 0; i0 < tasks; i0 += 32) {  // whole warps: the exponents are exchanged
+        for (int i0 = part * 32; i0 < tasks; i0 += team * 32) {  // whole warps: the exponents are exchanged
             const int i = i0 + lane, tok = i >> 3, at = kc * 128 + (i & 7) * 16;
             const float up = pow2(__shfl_sync(0xffffffffu, my_exp, tok & 31));
             if (i >= tasks) continue;
@@ -274,24 +280,26 @@ __device__ __forceinline__ void load_h(const float *src, int64_t step, int split
         for (int j = 0; j < V / 4; ++j) add4(v + 4 * j, src + q * step + 4 * j);
 }
 
-// The column operand of stage `kc` of a second product: ReLU of h, in terms.
+// The column operand of stage `kc` of a second product, ReLU of h in terms:
+// part `part` of `team`.
 template <bool E4M3>
 __device__ __forceinline__ void build_h(const FewArgs &p, uint8_t *tile, int A, int splits, int a0, int m, int kc,
-                                        int my_exp, int lane) {
+                                        int my_exp, int lane, int part, int team) {
     constexpr int V = E4M3 ? 16 : 8;  // values per 16-byte chunk
     const int tasks = m * 8, at = (kc * 8 + (lane & 7)) * V;
     const bool in = at < p.F;
     const float *h = p.h + (int64_t)a0 * p.F + at;
     const int64_t step = (int64_t)A * p.F;
     float next[V];
-    int i = lane;
+    const int stride = team * 32;
+    int i = part * 32 + lane;
     if (i < tasks && in) load_h<V>(h + (int64_t)(i >> 3) * p.F, step, splits, next);
-    for (int i0 = 0; i0 < tasks; i0 += 32, i += 32) {
+    for (int i0 = part * 32; i0 < tasks; i0 += stride, i += stride) {
         float v[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] = next[j];
         // the following task's values are on their way while this one's are cut
-        if (i + 32 < tasks && in) load_h<V>(h + (int64_t)((i + 32) >> 3) * p.F, step, splits, next);
+        if (i + stride < tasks && in) load_h<V>(h + (int64_t)((i + stride) >> 3) * p.F, step, splits, next);
         const int tok = i >> 3;
         const float up = E4M3 ? pow2(__shfl_sync(0xffffffffu, my_exp, tok & 31)) : 1.f;
         if (i >= tasks) continue;
@@ -402,7 +410,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) {
             for (int i = 0; i < kMaxStages; ++i) {
                 mbar_init(&s.full_a[i], 1);
-                mbar_init(&s.full_b[i], 1);
+                mbar_init(&s.full_b[i], kFull);
                 mbar_init(&s.empty[i], 1);
             }
             for (int i = 0; i < kMaxBufs; ++i) {
@@ -648,23 +656,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
     } else {
-        // No more builders than stages: the stages that a warp builds may not lie further apart than the
-        // ring is long, or it would take the parity of an older phase for that of the one it waits for.
+        // Stage i of an item is built by warp i mod `builders`, or by several where the item has fewer stages than
+        // there are warps.  A warp may take the parity of an older phase for that of the one it waits for once it is
+        // a whole lap of the ring ahead; it is not: the producer hands out an item after it has claimed the ring for
+        // all items before, which covers the first `stages` stages of this one, and from there on a warp's own
+        // stages lie `builders` <= `stages` apart.
         const int builders = min(kBuilders, stages), me = warp - 6;
-        int stage = 0;
-        uint32_t phase = 0, n = 0;
-        int count = 0;
+        int base = 0;  // ring stage and phase of the item's first stage
+        uint32_t base_phase = 0, n = 0;
         bool ok = true;
         while (ok) {
             const int item = next_item(s, n, lane, p.status);
             if (item < 0) break;
             const Item it = locate(w, item);
-            const int a0 = s.plan.g_first[it.g], m = s.plan.g_size[it.g];
+            const int a0 = s.plan.g_first[it.g], m = s.plan.g_size[it.g], len = it.k1 - it.k0;
             // One warp of the block asks memory whether the group's first product is complete, the others that one.
             if (it.second && !ready_cta(&s.ready[it.g])) {
                 int fine = 1;
                 if (lane == 0) {
-                    if (warp == 6) {
+                    if (me == 0) {
                         fine = wait_counter_geq(&p.ctr->done[it.g], 4 * w.tiles_h << w.log_h, p.status, 91);
                         if (fine) set_ready_cta(&s.ready[it.g]);
                     } else {
@@ -674,38 +684,42 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ok = __shfl_sync(0xffffffffu, fine, 0) != 0;
                 if (!ok) break;
             }
-            int my_exp = 0;  // 8-bit experts: exponent of token `lane`'s scale
-            bool ready = false;
-            for (int kc = it.k0; kc < it.k1; ++kc, ++count) {
-                if (count % builders == me) {
-                    if (!ready) {
-                        ready = true;
-                        if constexpr (E4M3) {
-                            if (lane < m) {
-                                if (it.second) {
-                                    float top = 0.f;
-                                    for (int q = 0; q < w.splits_h; ++q)
-                                        top += __uint_as_float(__ldcg(p.hmax + q * A + a0 + lane));
-                                    my_exp = scale_exponent(__float_as_uint(top));
-                                } else if (!X8) {
-                                    my_exp = scale_exponent(__ldcg(p.xmax + s.plan.token[a0 + lane]));
-                                }
-                            }
+            const int team = len >= builders ? 1 : builders / len;
+            int first = me / team;
+            const int part = me - first * team;
+            if (me >= builders) first = len;
+            if (first < len) {
+                int my_exp = 0;  // 8-bit experts: exponent of token `lane`'s scale
+                if constexpr (E4M3) {
+                    if (lane < m) {
+                        if (it.second) {
+                            float top = 0.f;
+                            for (int q = 0; q < w.splits_h; ++q)
+                                top += __uint_as_float(__ldcg(p.hmax + q * A + a0 + lane));
+                            my_exp = scale_exponent(__float_as_uint(top));
+                        } else if (!X8) {
+                            my_exp = scale_exponent(__ldcg(p.xmax + s.plan.token[a0 + lane]));
                         }
                     }
+                }
+                int stage = base + first;
+                uint32_t phase = base_phase;
+                for (int i = first; i < len; i += builders, stage += builders) {
+                    while (stage >= stages) stage -= stages, phase ^= 1u;
                     if (!mbar_wait(&s.empty[stage], phase ^ 1u, p.status, 92)) {
                         ok = false;
                         break;
                     }
                     uint8_t *tile = ring_b + stage * b_bytes;
-                    if (it.second) build_h<E4M3>(p, tile, A, w.splits_h, a0, m, kc, my_exp, lane);
-                    else build_x<E4M3, X8>(p, s.plan, tile, a0, m, kc, my_exp, lane);
+                    if (it.second) build_h<E4M3>(p, tile, A, w.splits_h, a0, m, it.k0 + i, my_exp, lane, part, team);
+                    else build_x<E4M3, X8>(p, s.plan, tile, a0, m, it.k0 + i, my_exp, lane, part, team);
                     fence_proxy_async_shared();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s.full_b[stage]);
+                    if (lane == 0) mbar_arrive_n(&s.full_b[stage], kFull / team);
                 }
-                if (++stage == stages) stage = 0, phase ^= 1u;
             }
+            base += len;
+            while (base >= stages) base -= stages, base_phase ^= 1u;
         }
     }
     tc_fence_before();
