@@ -171,7 +171,7 @@ cudaError_t router_typed(const FewArgs &p, int zero_ints, int want_xmax, cudaStr
 constexpr int kSimtThreads = 256;
 constexpr int kSimtBlocks = 2;  // per SM
 constexpr int kSimtWarps = kSimtThreads / 32;
-constexpr int kSimtRows = 8;  // weight rows of an item
+constexpr int kSimtRows = 8;  // weight rows of a team
 
 template <int TOK>
 struct SimtShared {
@@ -202,20 +202,20 @@ __device__ __forceinline__ float sum8(float (&v)[8], int lane) {
 }
 
 // red[j * 8 + r] = sum_k w[r][k] x_j[k], x_j the row token[j] (or j) of `in`,
-// over this warp's share of k (every eighth step of 32 V elements), for
-// kSimtRows rows of weights and m <= TOK tokens; rows past `rows_left` repeat
-// the last one.  U steps' weights are in flight together, as many as the
+// over this warp's share of k (steps first, first + TEAM, ... of 32 V elements),
+// for kSimtRows rows of weights and m <= TOK tokens; rows past `rows_left`
+// repeat the last one.  U steps' weights are in flight together, as many as the
 // registers beside the accumulators hold.
-template <typename W, typename X, int V, int TOK>
+template <typename W, typename X, int V, int TOK, int TEAM>
 __device__ __forceinline__ void simt_dots(const W *w, int rows_left, int K, const X *in, const int *token, int m,
-                                          int pitch, int warp, int lane, float *red) {
+                                          int pitch, int first, int lane, float *red) {
     float acc[TOK][kSimtRows];
 #pragma unroll
     for (int j = 0; j < TOK; ++j)
 #pragma unroll
         for (int r = 0; r < kSimtRows; ++r) acc[j][r] = 0.f;
-    constexpr int kStride = kSimtThreads * V, U = TOK == 4 ? (V == 1 ? 6 : 2) : (V == 1 ? 4 : 1);
-    for (int k0 = (warp * 32 + lane) * V; k0 < K; k0 += U * kStride) {
+    constexpr int kStride = TEAM * 32 * V, U = TOK == 4 ? (V == 1 ? 6 : 2) : (V == 1 ? 4 : 1);
+    for (int k0 = (first * 32 + lane) * V; k0 < K; k0 += U * kStride) {
         float wv[U][kSimtRows][V];
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -255,11 +255,19 @@ __device__ __forceinline__ void simt_dots(const W *w, int rows_left, int K, cons
     }
 }
 
-// A block takes an item: 8 weight rows of one expert, their length dealt out
-// to its 8 warps, for up to TOK tokens.  (Warps that take items of their own,
-// without the barriers, measured slower: their x rows come eight times as often.)
+// A block takes an item, for up to TOK tokens: 8 weight rows of one expert,
+// their length dealt out to its 8 warps; 64 rows, 8 to a warp, where the rows
+// are at most two steps long (20 tokens of 72 x 1284, 248 experts: 23 us, with 8
+// rows 40 us; on long rows warps of their own measured slower, their x rows
+// coming eight times as often).
+template <int V>
+__device__ __forceinline__ int simt_team(int K) {
+    return K <= 64 * V ? 1 : kSimtWarps;
+}
+
 // V: elements that a lane takes of a weight row at a time.
-template <typename W, typename X, int V, int TOK>
+// SHORT: W_in's or W_out's rows are (a kernel of its own: the other one's registers are all taken).
+template <typename W, typename X, int V, int TOK, bool SHORT>
 __global__ void __launch_bounds__(kSimtThreads, kSimtBlocks) few_experts_simt_kernel(const FewArgs p) {
     __shared__ SimtShared<TOK> s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -267,7 +275,9 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtBlocks) few_experts_simt_ke
     int next = 0;
     if (tid == 0) next = atomicAdd(&p.ctr->claim, 1);
     few_plan(p, s.plan, TOK, kSimtThreads);
-    const int tiles_h = (p.F + kSimtRows - 1) / kSimtRows, tiles_o = (p.d + kSimtRows - 1) / kSimtRows;
+    const int team_h = SHORT ? simt_team<V>(p.d) : kSimtWarps, team_o = SHORT ? simt_team<V>(p.F) : kSimtWarps;
+    const int rows_h = kSimtRows * kSimtWarps / team_h, rows_o = kSimtRows * kSimtWarps / team_o;  // of an item
+    const int tiles_h = (p.F + rows_h - 1) / rows_h, tiles_o = (p.d + rows_o - 1) / rows_o;
     const int groups = s.plan.groups, items_h = groups * tiles_h, items = items_h + groups * tiles_o;
     bool gates = false;
     for (;;) {
@@ -296,21 +306,29 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtBlocks) few_experts_simt_ke
         const int rest = r0 - q0 * (second ? groups : tiles_h);
         const int g = second ? rest : q0, tile = second ? q0 : rest;
         const int e = s.plan.g_expert[g], a0 = s.plan.g_first[g], m = s.plan.g_size[g];
-        const int row0 = tile * kSimtRows, rows = second ? p.d : p.F, K = second ? p.F : p.d;
-        const W *w = static_cast<const W *>(second ? p.w_out : p.w_in) + ((int64_t)e * rows + row0) * K;
-        if (second)
-            simt_dots<W, float, V, TOK>(w, rows - row0, K, p.h + (int64_t)a0 * p.F, nullptr, m, p.F, warp, lane,
-                                         s.red[warp]);
-        else
-            simt_dots<W, X, V, TOK>(w, rows - row0, K, static_cast<const X *>(p.x), s.plan.token + a0, m, p.d, warp,
-                                     lane, s.red[warp]);
+        const int team = SHORT ? (second ? team_o : team_h) : kSimtWarps;
+        const int tall = SHORT ? (second ? rows_o : rows_h) : kSimtRows;
+        const int row0 = tile * tall, rows = second ? p.d : p.F, K = second ? p.F : p.d;
+        const int mine = row0 + warp / team * kSimtRows;  // this team's first row
+        const W *w = static_cast<const W *>(second ? p.w_out : p.w_in) + ((int64_t)e * rows + mine) * K;
+        const X *x = static_cast<const X *>(p.x);
+        const float *h = p.h + (int64_t)a0 * p.F;
+        const int *list = s.plan.token + a0;
+        float *red = s.red[warp];
+        if (!SHORT || team == kSimtWarps) {
+            if (second) simt_dots<W, float, V, TOK, kSimtWarps>(w, rows - mine, K, h, nullptr, m, K, warp, lane, red);
+            else simt_dots<W, X, V, TOK, kSimtWarps>(w, rows - mine, K, x, list, m, K, warp, lane, red);
+        } else if (mine < rows) {
+            if (second) simt_dots<W, float, V, TOK, 1>(w, rows - mine, K, h, nullptr, m, K, 0, lane, red);
+            else simt_dots<W, X, V, TOK, 1>(w, rows - mine, K, x, list, m, K, 0, lane, red);
+        }
         __syncthreads();
-        if (tid < kSimtRows * m) {
-            const int j = tid / kSimtRows, row = row0 + tid % kSimtRows;
+        for (int i = tid; i < tall * m; i += kSimtThreads) {
+            const int j = i / tall, r = i - j * tall, row = row0 + r;
             if (row < rows) {
                 float v = 0.f;
-#pragma unroll
-                for (int q = 0; q < kSimtWarps; ++q) v += s.red[q][tid];
+#pragma unroll SHORT ? 1 : kSimtWarps
+                for (int q = 0; q < team; ++q) v += s.red[r / kSimtRows * team + q][j * kSimtRows + r % kSimtRows];
                 if (second) {
                     if (p.w_out_scale != nullptr) v *= p.w_out_scale[(int64_t)e * p.d + row];
                     p.o[(int64_t)(a0 + j) * p.d + row] = v;
@@ -329,8 +347,8 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtBlocks) few_experts_simt_ke
         if (second) {
             __syncthreads();
             if (s.last) {  // y of the tile's rows for every token
-                for (int i = tid; i < p.T * kSimtRows; i += kSimtThreads) {
-                    const int t = i / kSimtRows, row = row0 + i % kSimtRows;
+                for (int i = tid; i < p.T * tall; i += kSimtThreads) {
+                    const int t = i / tall, row = row0 + i - t * tall;
                     if (row >= p.d) continue;
                     float y = 0.f;
                     for (int c = 0; c < p.k; ++c) {
@@ -350,8 +368,10 @@ cudaError_t experts_simt(const FewArgs &p, cudaStream_t stream) {
     // of 4096 x 10000: 113 us, with 8 117 us); many: 8, so that weights are read for more tokens at a time (32
     // tokens top-2 of 1024 x 2048: 106 us, with 4 121 us).
     const bool few = p.T * p.k <= 16;
-    return launch_kernel(few ? few_experts_simt_kernel<W, X, V, 4> : few_experts_simt_kernel<W, X, V, 8>,
-                         dim3(device_sm_count() * kSimtBlocks), dim3(kSimtThreads), 0, stream, true, p);
+    const bool brief = p.d <= 64 * V || p.F <= 64 * V;
+    auto *kernel = few ? (brief ? few_experts_simt_kernel<W, X, V, 4, true> : few_experts_simt_kernel<W, X, V, 4, false>)
+                       : (brief ? few_experts_simt_kernel<W, X, V, 8, true> : few_experts_simt_kernel<W, X, V, 8, false>);
+    return launch_kernel(kernel, dim3(device_sm_count() * kSimtBlocks), dim3(kSimtThreads), 0, stream, true, p);
 }
 
 }  // namespace
