@@ -157,8 +157,8 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, int tpr, float *part) {
 // 2 units in the last place of the quotient, unless t is as close to the middle
 // between two e4m3 values: in the normal range those have the 20 low bits
 // 0x80000.  Eights with such a t, or with one below the normal range (2^-6), are
-// divided.  (These kernels are bound by instructions: 131072 x 1024 bfloat16
-// took 116 us with a division for every element, 81 us so.)
+// divided.  (131072 x 1024 bfloat16 took 116 us in the first kernel, which divided
+// every element; with this and its other steps 81 us.)
 struct Quantizer {
     float s, inv;
     bool tiny;  // 1 / s may overflow
