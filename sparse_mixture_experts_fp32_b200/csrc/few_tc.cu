@@ -161,12 +161,18 @@ __device__ __forceinline__ bool wait_ready_cta(const int *flag, DeviceStatus *st
     return true;
 }
 
+// A wait of a whole warp: all its lanes go on or all give up (a limit that ran out for some of them alone would leave
+// the others at a shuffle that those never reach).
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, DeviceStatus *st, int32_t where) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, st, where));
+}
+
 // Next item from the queue, for one warp; -1: no more, -2: the wait gave up.
 __device__ __forceinline__ int next_item(TcShared &s, uint32_t &n, int lane, DeviceStatus *status) {
     const int q = n % kQueue;
     const uint32_t parity = (n / kQueue) & 1u;
     ++n;
-    if (!mbar_wait(&s.q_full[q], parity, status, 81)) return -2;
+    if (!warp_wait(&s.q_full[q], parity, status, 81)) return -2;
     const int item = s.queue[q];
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.q_empty[q]);
@@ -572,9 +578,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ok = few_gates(p, s.plan, tid - 64, blockIdx.x == 0, [&] {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s.meet);
-                    const bool met = mbar_wait(&s.meet, turn, p.status, 94);
+                    const bool met = warp_wait(&s.meet, turn, p.status, 94);
                     turn ^= 1u;
-                    return __all_sync(0xffffffffu, met);
+                    return met;
                 });
                 if (!ok) break;
                 for (int t = blockIdx.x; t < p.T; t += gridDim.x)  // tokens that no expert keeps
@@ -599,7 +605,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
             for (int kc = it.k0; kc < it.k1; kc += kChain) {
-                if (!mbar_wait(&s.acc_full[buf], acc_phase, p.status, 90)) {
+                if (!warp_wait(&s.acc_full[buf], acc_phase, p.status, 90)) {
                     ok = false;
                     break;
                 }
@@ -676,10 +682,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (item < 0) break;
             const Item it = locate(w, item);
             const int a0 = s.plan.g_first[it.g], m = s.plan.g_size[it.g], len = it.k1 - it.k0;
-            // One warp of the block asks memory whether the group's first product is complete, the others that one.
-            if (it.second && !ready_cta(&s.ready[it.g])) {
+            // One warp of the block asks memory whether the group's first product is complete, the others that one; in a
+            // warp one lane does, for all (lanes that read the flag at different times must not part ways).
+            if (it.second) {
                 int fine = 1;
-                if (lane == 0) {
+                if (lane == 0 && !ready_cta(&s.ready[it.g])) {
                     if (me == 0) {
                         fine = wait_counter_geq(&p.ctr->done[it.g], 4 * w.tiles_h << w.log_h, p.status, 91);
                         if (fine) set_ready_cta(&s.ready[it.g]);
@@ -689,6 +696,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 ok = __shfl_sync(0xffffffffu, fine, 0) != 0;
                 if (!ok) break;
+                __syncwarp();  // what lane 0 has acquired, the others may read
             }
             const int team = len >= builders ? 1 : builders / len;
             int first = me / team;
@@ -712,7 +720,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 uint32_t phase = base_phase;
                 for (int i = first; i < len; i += builders, stage += builders) {
                     while (stage >= stages) stage -= stages, phase ^= 1u;
-                    if (!mbar_wait(&s.empty[stage], phase ^ 1u, p.status, 92)) {
+                    if (!warp_wait(&s.empty[stage], phase ^ 1u, p.status, 92)) {
                         ok = false;
                         break;
                     }
