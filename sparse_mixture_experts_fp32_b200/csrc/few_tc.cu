@@ -660,6 +660,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                            kept * w.splits_o - 1;
                 }
                 const uint32_t mask = __ballot_sync(0xffffffffu, last);
+                __syncwarp();  // the other warps' parts, which a lane has acquired, are read by all (a ballot orders no memory)
                 if (mask && live) {
                     if (p.k == 1) combine_row<1>(p, s.plan, w.splits_o, A, a0, mask, row);
                     else combine_row<2>(p, s.plan, w.splits_o, A, a0, mask, row);
