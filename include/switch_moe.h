@@ -324,7 +324,9 @@ switch_status_t switch_layer_bwd(const switch_dims_t *dims, const void *x, const
  * tokens reach.  Outputs and readings (ties, capacity, the order of slots,
  * aux) are those calls'; what differs:
  *  - the hidden activations are not rounded to bfloat16: y carries float32
- *    rounding only (about 1e-6 relative) beyond that of the given inputs;
+ *    rounding only (about 1e-6 relative) beyond that of the given inputs
+ *    (8-bit experts on tensor cores: a bfloat16 x below 2^-29 of its token's
+ *    largest |x| is rounded to 2^-37 of that);
  *  - the experts may be SWITCH_E4M3 (dims.dtype), with a float32 scale per
  *    output row (w_in_scale [N, F], w_out_scale [N, d]: W = q * scale); x is
  *    then bfloat16, or SWITCH_E4M3 too, with a scale per token (x_scale [T]).

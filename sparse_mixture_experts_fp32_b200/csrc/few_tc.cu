@@ -9,11 +9,15 @@
 // leaves room to spend columns on precision:
 //  - bfloat16 experts: a column per token for x; the float32 hidden value h is
 //    cut into three bfloat16 terms (exact), a column each;
-//  - 8-bit experts run as kind::f8f6f4, both operands e4m3: x in bfloat16 is cut
-//    into two e4m3 terms, h into five: each term rounds what the ones before it
-//    left, scaled by 16 more, so n terms hold 4 n bits.  A power of two per token
-//    brings its largest value into [128, 256).  The epilogue adds the columns of
-//    a token with their scales.  (x given in 8 bits is one column as it is.)
+//  - 8-bit experts run as kind::f8f6f4, weights as e4m3: x in bfloat16 is cut into
+//    three e5m2 terms (3 bits each, scaled by 8 more), h into five e4m3 ones (4
+//    bits each, scaled by 16 more): each term rounds what the ones before it left.
+//    A power of two per token brings its largest value into [2^14, 2^15) or
+//    [128, 256).  x takes the wider type, because its 8 bits need three terms of
+//    either type once a channel is 2^13 times another, and e5m2's exponents then
+//    hold every channel down to 2^-29 of the largest exactly (three e4m3 terms:
+//    2^-17).  The epilogue adds the columns of a token with their scales.  (x given
+//    in 8 bits is one column as it is.)
 // The tensor core truncates each addition to its float32 accumulator: over a
 // long row of weights that biases sums by up to 1e-5 (measured: K = 4096, 256
 // MMAs in a chain: 4e-6; 16 in a chain: 2.4e-7).  So an accumulator takes four
@@ -59,7 +63,7 @@ constexpr int kConsumers = 1 + 4 + kBuilders;  // warps that read the item queue
 
 template <bool E4M3, bool X8>
 struct Terms {
-    static constexpr int first = E4M3 ? (X8 ? 1 : 2) : 1;
+    static constexpr int first = E4M3 ? (X8 ? 1 : 3) : 1;
     static constexpr int second = E4M3 ? 5 : 3;
 };
 
@@ -84,9 +88,9 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
-// Instruction descriptor for kind::f8f6f4 with e4m3 A and B and an fp32 accumulator.
-__device__ __forceinline__ uint32_t idesc_e4m3_f32(int M, int N) {
-    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor for kind::f8f6f4 with e4m3 A, e4m3 or e5m2 B and an fp32 accumulator.
+__device__ __forceinline__ uint32_t idesc_e4m3_f32(int M, int N, bool b_e5m2) {
+    return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 __device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
@@ -179,24 +183,50 @@ __device__ __forceinline__ int next_item(TcShared &s, uint32_t &n, int lane, Dev
     return item;
 }
 
-// Power of two that brings a value with these bits into [128, 256) (0 stays,
-// tiny ones as far as 2^100), as its exponent; 1000: not finite.
-__device__ __forceinline__ int scale_exponent(uint32_t bits) {
+// Power of two that brings a value with these bits into [2^top, 2^(top + 1)) (0
+// stays, tiny ones as far as 2^126), as its exponent; 1000: not finite.
+constexpr int kTopX = 14, kTopH = 7;
+__device__ __forceinline__ int scale_exponent(uint32_t bits, int top) {
     const int e = (int)(bits >> 23) - 127;
     if (bits == 0) return 0;
-    return e == 128 ? 1000 : min(100, 7 - e);
+    return e == 128 ? 1000 : min(126, top - e);
 }
 __device__ __forceinline__ float pow2(int k) { return __int_as_float((127 + min(127, k)) << 23); }  // k >= -126
 __device__ __forceinline__ float unscale(int k) { return k == 1000 ? __int_as_float(0x7fc00000) : pow2(-k); }
 
-// 16 values of at most 256 -> TERMS rows of 16 e4m3 bytes, term i holding what
+// 16 bfloat16 values below 2^15 -> three rows of 16 e5m2 bytes, term i holding
+// what the terms before it left, times 8^i.  They are cut in float16, two values
+// at a time, which holds every difference exactly: all of the 8 bits of a value
+// down to 2^-15, and 2^-23 of any smaller one.
+__device__ __forceinline__ void store_e5m2_terms(uint8_t *tile, int row0, int chunk, const float (&v)[16]) {
+    uint32_t w[3][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        __half2 left = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {
+            const __nv_fp8x2_storage_t q = __nv_cvt_halfraw2_to_fp8x2((__half2_raw)left, __NV_SATFINITE, __NV_E5M2);
+            if (i & 1) w[t][i >> 1] |= (uint32_t)q << 16;
+            else w[t][i >> 1] = q;
+            if (t < 2)
+                left = __hmul2(__hsub2(left, __half2(__nv_cvt_fp8x2_to_halfraw2(q, __NV_E5M2))), __float2half2_rn(8.f));
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+        const int row = row0 + t;
+        *reinterpret_cast<uint4 *>(tile + row * 128 + ((chunk ^ (row & 7)) << 4)) =
+            make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+    }
+}
+
+// 16 values of at most 256 -> five rows of 16 e4m3 bytes, term i holding what
 // the terms before it left, times 16^i.  The terms are cut in float16, two
 // values at a time: its 11 bits hold what three terms do exactly (the third is
 // what the first two leave of them), and what it leaves of v, times 16^3, makes
-// the fourth and fifth (2 terms: v is a bfloat16, which float16 holds exactly).
-template <int TERMS>
+// the fourth and fifth.
 __device__ __forceinline__ void store_e4m3_terms(uint8_t *tile, int row0, int chunk, const float (&v)[16]) {
-    static_assert(TERMS == 2 || TERMS == 5, "x, h");
+    constexpr int TERMS = 5;
     uint32_t w[TERMS][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -273,7 +303,7 @@ __device__ __forceinline__ void build_x(const FewArgs &p, const FewPlan &s, uint
                     }
                 }
             }
-            store_e4m3_terms<2>(tile, tok * 2, i & 7, v);
+            store_e5m2_terms(tile, tok * 3, i & 7, v);
         }
     }
 }
@@ -318,7 +348,7 @@ __device__ __forceinline__ void build_h(const FewArgs &p, uint8_t *tile, int A, 
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] = !in || v[j] < 0.f ? 0.f : v[j] * up;  // NaN stays NaN
         if constexpr (E4M3) {
-            store_e4m3_terms<5>(tile, tok * 5, lane & 7, v);
+            store_e4m3_terms(tile, tok * 5, lane & 7, v);
         } else {
             uint16_t t[3][8];
 #pragma unroll
@@ -340,8 +370,8 @@ __device__ __forceinline__ void build_h(const FewArgs &p, uint8_t *tile, int A, 
     }
 }
 
-// v[j] += the accumulator's value for token j (its terms joined), m tokens.
-template <bool E4M3, int TERMS>
+// v[j] += the accumulator's value for token j (its terms joined, each STEP times the one before it), m tokens.
+template <int TERMS, int STEP>
 __device__ __forceinline__ void add_accumulator(uint32_t taddr, int m, float (&v)[kGroup]) {
 #pragma unroll
     for (int b = 0; b < kGroup / 8; ++b) {
@@ -356,7 +386,7 @@ __device__ __forceinline__ void add_accumulator(uint32_t taddr, int m, float (&v
 #pragma unroll
             for (int t = TERMS - 1; t >= 0; --t) {
                 const int col = j * TERMS + t;
-                a = a * (E4M3 ? 0.0625f : 1.f) + __uint_as_float(r[col / 8][col % 8]);
+                a = a * (1.f / STEP) + __uint_as_float(r[col / 8][col % 8]);
             }
             v[b * 8 + j] += a;
         }
@@ -524,7 +554,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const Item it = locate(w, item);
                 const int cols = s.plan.g_size[it.g] * (it.second ? Terms<E4M3, X8>::second : Terms<E4M3, X8>::first);
                 const int N = (cols + 15) / 16 * 16;
-                const uint32_t idesc = E4M3 ? idesc_e4m3_f32(128, N) : idesc_bf16_f32(128, N);
+                const uint32_t idesc = E4M3 ? idesc_e4m3_f32(128, N, !X8 && !it.second) : idesc_bf16_f32(128, N);
                 for (int kc = it.k0; ok && kc < it.k1;) {
                     if (!mbar_wait(&s.acc_empty[buf], acc_phase ^ 1u, p.status, 86)) {
                         ok = false;
@@ -601,7 +631,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (live) scale = __ldg((it.second ? p.w_out_scale : p.w_in_scale) + (int64_t)e * rows + row);
                 if (!it.second && lane < m) {
                     const int t = s.plan.token[a0 + lane];
-                    own = X8 ? __ldg(p.x_scale + t) : unscale(scale_exponent(__ldcg(p.xmax + t)));
+                    own = X8 ? __ldg(p.x_scale + t) : unscale(scale_exponent(__ldcg(p.xmax + t), kTopX));
                 }
             }
             for (int kc = it.k0; kc < it.k1; kc += kChain) {
@@ -611,8 +641,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t at = lanes + (uint32_t)(buf * acc_cols);
-                if (it.second) add_accumulator<E4M3, Terms<E4M3, X8>::second>(at, m, v);
-                else add_accumulator<E4M3, Terms<E4M3, X8>::first>(at, m, v);
+                if (it.second) add_accumulator<Terms<E4M3, X8>::second, E4M3 ? 16 : 1>(at, m, v);
+                else add_accumulator<Terms<E4M3, X8>::first, E4M3 ? 8 : 1>(at, m, v);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.acc_empty[buf]);
@@ -624,7 +654,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (it.second && lane < m) {
                     float top = 0.f;
                     for (int q = 0; q < w.splits_h; ++q) top += __uint_as_float(__ldcg(p.hmax + q * A + a0 + lane));
-                    own = unscale(scale_exponent(__float_as_uint(top)));
+                    own = unscale(scale_exponent(__float_as_uint(top), kTopH));
                 }
             }
             float *out = it.second ? p.o + ((int64_t)it.split * A + a0) * p.d : p.h + ((int64_t)it.split * A + a0) * p.F;
@@ -711,9 +741,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             float top = 0.f;
                             for (int q = 0; q < w.splits_h; ++q)
                                 top += __uint_as_float(__ldcg(p.hmax + q * A + a0 + lane));
-                            my_exp = scale_exponent(__float_as_uint(top));
+                            my_exp = scale_exponent(__float_as_uint(top), kTopH);
                         } else if (!X8) {
-                            my_exp = scale_exponent(__ldcg(p.xmax + s.plan.token[a0 + lane]));
+                            my_exp = scale_exponent(__ldcg(p.xmax + s.plan.token[a0 + lane]), kTopX);
                         }
                     }
                 }
