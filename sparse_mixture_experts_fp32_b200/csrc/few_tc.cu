@@ -222,9 +222,11 @@ __device__ __forceinline__ void store_e5m2_terms(uint8_t *tile, int row0, int ch
 
 // 16 values of at most 256 -> five rows of 16 e4m3 bytes, term i holding what
 // the terms before it left, times 16^i.  The terms are cut in float16, two
-// values at a time: its 11 bits hold what three terms do exactly (the third is
-// what the first two leave of them), and what it leaves of v, times 16^3, makes
-// the fourth and fifth.
+// values at a time: its 11 bits are what three terms hold, down to values of 2^-7
+// (below, the third term is at the end of e4m3's range and leaves some); what it
+// leaves of v and what they leave of it, times 16^3, make the fourth and fifth.
+// So a value is off by 2^-19 of itself, or by half of the fifth term's smallest
+// step, 2^-26 (2^-33 of a row's largest), where that is more.
 __device__ __forceinline__ void store_e4m3_terms(uint8_t *tile, int row0, int chunk, const float (&v)[16]) {
     constexpr int TERMS = 5;
     uint32_t w[TERMS][4];
@@ -235,11 +237,11 @@ __device__ __forceinline__ void store_e4m3_terms(uint8_t *tile, int row0, int ch
 #pragma unroll
         for (int t = 0; t < TERMS; ++t) {
             if (t == 3)
-                left = __floats2half2_rn((v[2 * i] - top.x) * 4096.f, (v[2 * i + 1] - top.y) * 4096.f);
+                left = __hadd2(left, __floats2half2_rn((v[2 * i] - top.x) * 4096.f, (v[2 * i + 1] - top.y) * 4096.f));
             const __nv_fp8x2_storage_t q = __nv_cvt_halfraw2_to_fp8x2((__half2_raw)left, __NV_SATFINITE, __NV_E4M3);
             if (i & 1) w[t][i >> 1] |= (uint32_t)q << 16;
             else w[t][i >> 1] = q;
-            if (t + 1 < TERMS && t != 2)
+            if (t + 1 < TERMS)
                 left = __hmul2(__hsub2(left, __half2(__nv_cvt_fp8x2_to_halfraw2(q, __NV_E4M3))), __float2half2_rn(16.f));
         }
     }

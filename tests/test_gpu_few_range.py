@@ -79,3 +79,39 @@ def test_large_channels_within_a_token(T, d, F, N, k, power, zeros):
     want = plain(p, k, T)
     check(run(p, k), want, k)
     check(run(p, k, flags=sm.SWITCH_FLAG_SIMT_FFN), want, k)
+
+
+def in_three(v):
+    """float32 values as three bfloat16 ones of 8 bits each, all of v's sign, whose sum is v."""
+    hi = (v.view(torch.int32) & -65536).view(F32)
+    rest = v - hi
+    mid = (rest.view(torch.int32) & -65536).view(F32)
+    return hi, mid, rest - mid
+
+
+def hidden(seed, T, w, d, large):
+    """x and the selections whose hidden row is v (24 bits, in [1, 2)) at 0..59 and 2^large at 63, and v."""
+    v = 1 + uniform(seed, T, 60)
+    x = torch.zeros(T, d, device="cuda")
+    at = [0, d // 2, d - 64]  # in parts of their own where a row is cut
+    into = []
+    for a, piece in zip(at, in_three(v)):
+        x[:, a:a + 60] = piece
+        into += [(j, a + j) for j in range(60)]
+    x[:, d - 1] = 2.0 ** large
+    into.append((63, d - 1))
+    return x.to(F32 if w == "f32" else BF16), into, v.double()
+
+
+@pytest.mark.parametrize("T", [1, 5, 33])
+@pytest.mark.parametrize("w", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("d,large", [(256, 0), (256, 9), (256, 14), (2112, 0), (2112, 12), (2112, 19)])
+def test_hidden_values_are_held_beside_large_ones(T, w, d, large):
+    """A hidden value of 2^large that no weight of the second product takes (and its x, which rounds the smallest
+    pieces of v to 2^-37 of it)."""
+    F = 64
+    x, into, v = hidden(400 + large, T, w, d, large)
+    y = through(w, x, F, into, [(j, j) for j in range(60)], d)
+    floor = (2.0 ** -33 + 3 * 2.0 ** -37) * 2.0 ** large if w == "e4m3" else 0.0
+    assert ((y[:, :60].double() - v).abs() <= HELD[w] * 1.01 * v + floor).all()
+    assert (y[:, 60:] == 0).all()
