@@ -33,7 +33,8 @@ struct FewArgs {
     DeviceStatus *status;
     FewCounters *ctr;
     uint32_t *xmax;    // [T] bits of max |x| (8-bit experts with bfloat16 x)
-    uint32_t *hmax;    // [splits][A] bits of max |partial sum| of a pair's hidden row (tensor cores)
+    uint32_t *hmax;    // [splits][A] bits of the largest positive partial sum of a pair's hidden row (tensor cores); their
+                       // sum over the parts is at least the row's largest value after ReLU
     int32_t *parts;    // [ceil(d / 128) * 4][T] finished parts of 32 values of a token's y (tensor cores)
     float *logits;     // [T][N]
     float *h;          // [splits][A][F] first product (before ReLU where it is split)

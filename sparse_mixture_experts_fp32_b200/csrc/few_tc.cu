@@ -667,7 +667,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if constexpr (E4M3) {
                     u = u * __shfl_sync(0xffffffffu, own, j) * scale;
                     if (!it.second) {
-                        const uint32_t top = __reduce_max_sync(0xffffffffu, live ? __float_as_uint(u) & 0x7fffffffu : 0u);
+                        // Negative values are left out: ReLU removes them, or the sum with other parts is less than
+                        // theirs.  (A NaN's bits are above all.)
+                        const uint32_t top =
+                            __reduce_max_sync(0xffffffffu, live && !(u < 0.f) ? __float_as_uint(u) & 0x7fffffffu : 0u);
                         if (lane == 0) atomicMax(p.hmax + it.split * A + a0 + j, top);
                     }
                 }

@@ -115,3 +115,24 @@ def test_hidden_values_are_held_beside_large_ones(T, w, d, large):
     floor = (2.0 ** -33 + 3 * 2.0 ** -37) * 2.0 ** large if w == "e4m3" else 0.0
     assert ((y[:, :60].double() - v).abs() <= HELD[w] * 1.01 * v + floor).all()
     assert (y[:, 60:] == 0).all()
+
+
+@pytest.mark.parametrize("T", [1, 5, 33])
+@pytest.mark.parametrize("w", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("d", [256, 2112])
+@pytest.mark.parametrize("large", [10, 24, 60])
+def test_what_relu_removes_takes_no_bits(T, w, d, large):
+    """A pre-activation of -2^large in the same row."""
+    F = 64
+    x, into, v = hidden(500 + large, T, w, d, 0)
+    x[:, d - 2] = 1
+    p_in, p_out = select(F, d, into[:-1], F32), select(d, F, [(j, j) for j in range(60)], WEIGHTS[w])
+    p_in[0, 62, d - 2] = -1.0 if w == "e4m3" else -(2.0 ** large)
+    p_out[0, :, 62] = 1  # it would show everywhere
+    p = dict(x=x, w_r=torch.zeros(1, d, device="cuda"), logit_bias=None, w_in=p_in.to(WEIGHTS[w]), w_out=p_out)
+    if w == "e4m3":
+        p["w_in_scale"], p["w_out_scale"] = torch.ones(1, F, device="cuda"), torch.ones(1, d, device="cuda")
+        p["w_in_scale"][0, 62] = 2.0 ** large
+    y = run(p, 1, T)["y"]
+    assert ((y[:, :60].double() - v).abs() <= HELD[w] * 1.01 * v).all()
+    assert (y[:, 60:] == 0).all()
