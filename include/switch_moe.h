@@ -366,8 +366,11 @@ switch_status_t switch_layer_fwd_few(const switch_dims_t *dims, int32_t top_k, c
  *   v_j  = s_j * rstd * weight_j       in float32
  *   out  = v rounded to out_dtype; for SWITCH_E4M3: scale = max_j |v_j| / 448,
  *          out_j = e4m3(v_j / scale)   (nearest, ties to even)
- * A row of zeros has scale 0 and zeros; a row with a NaN or an infinity has a
- * scale (or outputs) that are not finite, and no other row does. */
+ * A row of zeros has scale 0 and zeros (with eps = 0 too, where its rstd is
+ * infinite and switch_norm_bwd's gradients of it are not finite); a row with a
+ * NaN or an infinity has a scale (or outputs) that are not finite, and no other
+ * row does.  Finite rows may have any size: where squares leave float32's range
+ * they are summed scaled (rstd itself is rounded to float32's range). */
 typedef struct {
     int64_t T;              /* rows; 0 <= T < 2^31 */
     int32_t d_model;        /* d, 1..8192 (any; multiples of 8 are faster) */

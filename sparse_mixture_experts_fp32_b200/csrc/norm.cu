@@ -23,10 +23,11 @@
 //
 // Measured on a B200 (copy bandwidth 6549 GB/s): 131072 x 1024 bfloat16 +
 // float32 -> bfloat16 194 us (6.9 TB/s), its gradient 304 us (6.2 TB/s);
-// 8192 x 768 float32 + float32 -> 8 bits 16.1 us (5.1 TB/s); 131072 x 1024
+// 8192 x 768 float32 + float32 -> 8 bits 16.2 us (5.0 TB/s); 131072 x 1024
 // bfloat16 to 8 bits 81 us (5.0 TB/s).
 #include <cuda_fp8.h>
 
+#include <cfloat>
 #include <type_traits>
 
 #include "common.cuh"
@@ -187,6 +188,14 @@ struct Quantizer {
     }
 };
 
+// Whether the mean of a row's squares (with eps) is beyond float32's range
+// (values from about 1e19 up), or so small that squares may have lost bits (below
+// about 1e-15): the row is then scaled by a power of two and summed once more.
+__device__ __forceinline__ bool beyond_squares(float mean) {
+    constexpr uint32_t least = 27u << 23;  // 2^-100; a NaN's bits are above an infinity's
+    return __float_as_uint(mean) - least >= (255u << 23) - least;
+}
+
 template <typename R, typename D, typename O, bool ODD>
 __global__ void __launch_bounds__(1024)
     norm_fwd_kernel(const R *residual, const D *delta, const float *__restrict__ weight, R *sum, O *out,
@@ -220,8 +229,26 @@ __global__ void __launch_bounds__(1024)
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) ss = fmaf(s[k], s[k], ss);
-    const float r = __frcp_rn(__fsqrt_rn(row_sum(ss, tpr, part[0]) / (float)d + eps));
-    if (live && threadIdx.x == 0 && rstd != nullptr) rstd[t] = r;
+    const float mean = row_sum(ss, tpr, part[0]) / (float)d + eps;
+    float r = __frcp_rn(__fsqrt_rn(mean)), r_stored = r;
+    if (__builtin_expect(beyond_squares(mean), 0)) {  // (the same in all threads that share a row or a barrier)
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(s[k]) & 0x7fffffffu);
+        top = row_max(top, tpr, part[1]);
+        if (top < 0x7f800000u) {  // (a row with a NaN or an infinity stays as it is)
+            const float m = fmaxf(__uint_as_float(top), __fsqrt_rn(eps));
+            const int down = m > 0.f ? -ilogbf(m) : 0;
+            const float a = scalbnf(1.f, down / 2), b = scalbnf(1.f, down - down / 2);
+            ss = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s[k] = s[k] * a * b, ss = fmaf(s[k], s[k], ss);
+            r = __frcp_rn(__fsqrt_rn(row_sum(ss, tpr, part[0]) / (float)d + eps * a * b * a * b));
+            r_stored = r * a * b;
+            if (m == 0.f) r = 0.f;  // zeros without an eps: 0 beside an infinite rstd
+        }
+    }
+    if (live && threadIdx.x == 0 && rstd != nullptr) rstd[t] = r_stored;
     if (j < d) {
         float w[8];
         load_weight<ODD>(weight, j, d, w);
@@ -427,7 +454,8 @@ int eights(int d) { return d % 8 == 0 ? d / 8 : (d + 7 + 7) / 8; }
 template <typename R, typename D, typename O>
 void norm_fwd_typed(const switch_norm_dims_t &n, const void *residual, const void *delta, const float *weight,
                     void *sum, void *out, float *scale, float *rstd, cudaStream_t stream) {
-    const RowShape s = shape_of(eights(n.d_model), 1);
+    RowShape s = shape_of(eights(n.d_model), 1);
+    if (s.tpr > 32) s.rows = 1;  // (rows that share a barrier would have to agree on a second sum)
     const dim3 grid((unsigned)((n.T + s.rows - 1) / s.rows)), block(s.tpr, s.rows);
     auto *kernel = n.d_model % 8 == 0 ? norm_fwd_kernel<R, D, O, false> : norm_fwd_kernel<R, D, O, true>;
     kernel<<<grid, block, 0, stream>>>(static_cast<const R *>(residual), static_cast<const D *>(delta), weight,
