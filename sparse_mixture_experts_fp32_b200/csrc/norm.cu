@@ -37,9 +37,6 @@ namespace switchmoe {
 namespace {
 
 constexpr float kE4m3Max = 448.f;
-#ifndef QI
-#define QI 4
-#endif
 struct None {};  // no delta
 
 // Eight elements of a row of d, from element j on.  ODD: j may be up to 7
