@@ -494,10 +494,13 @@ def route_top2(x, w_r, capacity=None, capacity_factor=None, logit_bias=None, d_f
 
 def layer_bwd(fwd: dict, x, w_r, w_in, w_out, dy, g_aux: float = 0.0, logit_bias=None, stream=None):
     """Gradients of sum(y * dy) + g_aux * aux after ``layer_fwd(..., flags=SWITCH_FLAG_TRAINING)``
-    (whose result dict, with its workspace, is ``fwd``).  Returns dx, dw_r, dbias
-    (None without a logit bias), dw_in, dw_out, all float32."""
+    (whose result dict, with its workspace, is ``fwd``; a top-2 forward has no backward pass).
+    Returns dx, dw_r, dbias (None without a logit bias), dw_in, dw_out, all float32."""
     import torch
     T, dm = x.shape
+    if tuple(fwd["expert"].shape) != (T,):
+        raise ValueError(f"fwd must be layer_fwd's result for x, one expert per token: expert is "
+                         f"{list(fwd['expert'].shape)} for {T} tokens")
     N, F, _ = w_in.shape
     dev = x.device
     d = layer_dims(x, w_in, capacity=fwd["capacity"], flags=fwd.get("flags", SWITCH_FLAG_TRAINING))
@@ -844,7 +847,8 @@ def block_fwd(residual, norm_weight, w_r, w_in, w_out, delta=None, eps: float = 
 
 def block_bwd(fwd: dict, norm_weight, w_r, w_in, w_out, dy, dsum=None, g_aux: float = 0.0, logit_bias=None,
               stream=None):
-    """Gradients of sum(y * dy) + sum(s * dsum) + g_aux * aux after ``block_fwd(..., flags=SWITCH_FLAG_TRAINING)``:
+    """Gradients of sum(y * dy) + sum(s * dsum) + g_aux * aux after ``block_fwd(..., flags=SWITCH_FLAG_TRAINING)`` with
+    top_k 1 (the top-2 layer has no backward pass, and is refused):
     layer_bwd's dw_r, dbias, dw_in, dw_out, with dresidual (of residual and delta alike) and dnorm_weight, float32."""
     g = layer_bwd(fwd, fwd["x"], w_r, w_in, w_out, dy, g_aux, logit_bias, stream)
     n = norm_bwd(fwd["sum"], norm_weight, fwd["rstd"], g.pop("dx"), dsum=dsum, stream=stream)
