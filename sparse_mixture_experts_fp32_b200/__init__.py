@@ -828,20 +828,24 @@ def block_fwd(residual, norm_weight, w_r, w_in, w_out, delta=None, eps: float = 
     always do, with x in 8 bits), others through switch_layer_fwd / switch_layer_fwd_top2.  Returns the layer's
     dict with sum (residual where there is no delta), x, x_scale and rstd besides."""
     import torch
+    if stream is not None:
+        with _under(stream, residual.device):
+            return block_fwd(residual, norm_weight, w_r, w_in, w_out, delta, eps, top_k, capacity, capacity_factor,
+                             logit_bias, w_in_scale, w_out_scale, flags)
     few = w_in.dtype == torch.float8_e4m3fn or (residual.shape[0] <= SWITCH_FEW_MAX_TOKENS
                                                 and (flags & ~SWITCH_FLAG_SIMT_FFN) == 0)
     if not few and top_k not in (1, 2):
         raise ValueError("top_k must be 1 or 2")
-    n = norm_fwd(residual, norm_weight, delta=delta, eps=eps, out_dtype=w_in.dtype, stream=stream)
+    n = norm_fwd(residual, norm_weight, delta=delta, eps=eps, out_dtype=w_in.dtype)
     x = n["out"]
     if few:
         if capacity is None and capacity_factor is None:
             raise ValueError("give capacity or capacity_factor")
         r = layer_fwd_few(x, w_r, w_in, w_out, top_k, capacity, capacity_factor, logit_bias, n["scale"], w_in_scale,
-                          w_out_scale, flags, stream=stream)
+                          w_out_scale, flags)
     else:
         r = (layer_fwd if top_k == 1 else layer_fwd_top2)(x, w_r, w_in, w_out, capacity, capacity_factor, logit_bias,
-                                                          flags, stream=stream)
+                                                          flags)
     return dict(r, sum=residual if delta is None else n["sum"], x=x, x_scale=n["scale"], rstd=n["rstd"])
 
 
@@ -850,6 +854,9 @@ def block_bwd(fwd: dict, norm_weight, w_r, w_in, w_out, dy, dsum=None, g_aux: fl
     """Gradients of sum(y * dy) + sum(s * dsum) + g_aux * aux after ``block_fwd(..., flags=SWITCH_FLAG_TRAINING)`` with
     top_k 1 (the top-2 layer has no backward pass, and is refused):
     layer_bwd's dw_r, dbias, dw_in, dw_out, with dresidual (of residual and delta alike) and dnorm_weight, float32."""
-    g = layer_bwd(fwd, fwd["x"], w_r, w_in, w_out, dy, g_aux, logit_bias, stream)
-    n = norm_bwd(fwd["sum"], norm_weight, fwd["rstd"], g.pop("dx"), dsum=dsum, stream=stream)
+    if stream is not None:
+        with _under(stream, dy.device):  # dx, which dies here, is allocated on the stream that it is used on
+            return block_bwd(fwd, norm_weight, w_r, w_in, w_out, dy, dsum, g_aux, logit_bias)
+    g = layer_bwd(fwd, fwd["x"], w_r, w_in, w_out, dy, g_aux, logit_bias)
+    n = norm_bwd(fwd["sum"], norm_weight, fwd["rstd"], g.pop("dx"), dsum=dsum)
     return dict(g, dresidual=n["dresidual"], dnorm_weight=n["dweight"])

@@ -33,3 +33,41 @@ def test_gradients_of_a_top2_forward_are_refused(no_calls):
             sm.layer_bwd(fwd, x, w_r, w_in, w_out, dy)
         with pytest.raises(ValueError, match="one expert per token"):
             sm.block_bwd(fwd, torch.ones(D), w_r, w_in, w_out, dy)
+
+
+def test_blocks_allocate_on_the_stream_that_they_use(monkeypatch):
+    """With stream=, everything within runs with that stream as the current one, and is given none."""
+    now, seen = [], []
+
+    class under:
+        def __init__(self, stream, device):
+            self.stream = stream
+
+        def __enter__(self):
+            now.append(self.stream)
+
+        def __exit__(self, *a):
+            now.pop()
+
+    def record(name, result):
+        def call(*a, stream=None, **k):
+            seen.append((name, now[-1] if now else None, stream))
+            return dict(result)
+        return call
+
+    w_r, w_in, w_out = weights()
+    x, rows = torch.zeros(100, D, dtype=torch.bfloat16), torch.zeros(100, D)
+    monkeypatch.setattr(sm, "_under", under)
+    monkeypatch.setattr(sm, "norm_fwd", record("norm_fwd", dict(out=x, scale=None, sum=rows, rstd=rows[:, 0])))
+    monkeypatch.setattr(sm, "norm_bwd", record("norm_bwd", dict(dresidual=rows, dweight=rows[0])))
+    monkeypatch.setattr(sm, "layer_bwd", record("layer_bwd", dict(dx=rows)))
+    for name in ("layer_fwd", "layer_fwd_top2"):
+        monkeypatch.setattr(sm, name, record(name, dict(y=rows)))
+    for k, layer in ((1, "layer_fwd"), (2, "layer_fwd_top2")):
+        seen.clear()
+        f = sm.block_fwd(rows, rows[0], w_r, w_in, w_out, capacity=8, top_k=k, stream="side")
+        assert seen == [("norm_fwd", "side", None), (layer, "side", None)]
+    seen.clear()
+    sm.block_bwd(f, rows[0], w_r, w_in, w_out, rows, stream="side")
+    assert seen == [("layer_bwd", "side", None), ("norm_bwd", "side", None)]
+    assert not now
