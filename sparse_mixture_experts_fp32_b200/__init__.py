@@ -24,6 +24,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 from pathlib import Path
 
 _PKG = Path(__file__).resolve().parent
@@ -725,8 +726,9 @@ class FewLayer:
     """The layer for up to 64 tokens over one set of weights (switch_layer_fwd_few): the handle that a serving
     program keeps.  w_r [N, d] float32; w_in [N, F, d] and w_out [N, d, F] float32, bfloat16 or float8_e4m3fn, the
     last with w_in_scale [N, F] and w_out_scale [N, d] (quantize_rows makes both).  ``capacity`` None keeps every
-    token.  The tensors are held and read at each call; calls may run on several streams at once (each has a
-    workspace of its own unless it is given one)."""
+    token.  The tensors are held and read at each call, so they may be updated in place; the handle's attributes
+    cannot be set (other sizes, weights or a capacity are another handle).  Calls may run on several streams at once
+    (each has a workspace of its own unless it is given one)."""
 
     def __init__(self, w_r, w_in, w_out, top_k: int = 1, capacity=None, capacity_factor=None, logit_bias=None,
                  w_in_scale=None, w_out_scale=None, flags: int = 0):
@@ -738,53 +740,71 @@ class FewLayer:
         e4m3 = w_in.dtype == torch.float8_e4m3fn
         if e4m3 != (w_in_scale is not None) or e4m3 != (w_out_scale is not None):
             raise ValueError("float8_e4m3fn experts, and they only, have w_in_scale and w_out_scale")
-        f32 = (torch.float32,)
-        _want("w_in", w_in, (N, F, dm), (torch.float32, torch.bfloat16, torch.float8_e4m3fn), dev)
-        _want("w_out", w_out, (N, dm, F), (w_in.dtype,), dev)
-        _want("w_r", w_r, (N, dm), f32, dev)
-        _want("logit_bias", logit_bias, (N,), f32, dev)
-        _want("w_in_scale", w_in_scale, (N, F), f32, dev)
-        _want("w_out_scale", w_out_scale, (N, dm), f32, dev)
+        self._w_r, self._w_in, self._w_out, self._logit_bias = w_r, w_in, w_out, logit_bias
+        self._w_in_scale, self._w_out_scale = w_in_scale, w_out_scale
+        self._num_experts, self._d_ff, self._d_model, self._device, self._dtype = N, F, dm, dev, w_in.dtype
+        if not e4m3 and w_in.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"w_in must be float32, bfloat16 or float8_e4m3fn, got {w_in.dtype}")
+        self._held, self._memory = self._weights(), None
         if capacity is not None and capacity_factor is not None:
             raise ValueError("give capacity or capacity_factor, not both")
-        self.w_r, self.w_in, self.w_out, self.logit_bias = w_r, w_in, w_out, logit_bias
-        self.w_in_scale, self.w_out_scale = w_in_scale, w_out_scale
-        self.top_k, self.capacity, self.capacity_factor, self.flags = int(top_k), capacity, capacity_factor, int(flags)
-        self.num_experts, self.d_ff, self.d_model, self.device, self.dtype = N, F, dm, dev, w_in.dtype
+        self._top_k, self._capacity, self._capacity_factor, self._flags = int(top_k), capacity, capacity_factor, int(flags)
         self._x_types = {False: (torch.bfloat16,) if e4m3 else (w_in.dtype,), True: (torch.float8_e4m3fn,)}
         self._sizes = {}  # at most 65 entries: more tokens are refused
         self._dims(1)  # refuses sizes that no call could run with
+
+    def _weights(self):
+        """Checks the tensors; returns their addresses, in the C function's order."""
+        import torch
+        N, F, dm, dev, f32 = self._num_experts, self._d_ff, self._d_model, self._device, (torch.float32,)
+        return (_want("w_r", self._w_r, (N, dm), f32, dev),
+                _want("logit_bias", self._logit_bias, (N,), f32, dev),
+                _want("w_in", self._w_in, (N, F, dm), (self._dtype,), dev),
+                _want("w_in_scale", self._w_in_scale, (N, F), f32, dev),
+                _want("w_out", self._w_out, (N, dm, F), (self._dtype,), dev),
+                _want("w_out_scale", self._w_out_scale, (N, dm), f32, dev))
 
     def _dims(self, T):
         """(dims, their address, workspace bytes) of calls with T tokens."""
         got = self._sizes.get(T)
         if got is None:
-            if self.capacity is not None:
-                C = int(self.capacity)
-            elif self.capacity_factor is not None:
-                C = _resolve_capacity(T, self.num_experts, None, self.capacity_factor)
+            if self._capacity is not None:
+                C = int(self._capacity)
+            elif self._capacity_factor is not None:
+                C = _resolve_capacity(T, self._num_experts, None, self._capacity_factor)
             else:
                 C = max(1, T)
-            d = dims(T, self.d_model, self.d_ff, self.num_experts, C, _code(self.dtype), self.flags)
-            got = self._sizes[T] = (d, ctypes.byref(d), switch_few_workspace_size(d, self.top_k))
+            d = dims(T, self._d_model, self._d_ff, self._num_experts, C, _code(self._dtype), self._flags)
+            got = self._sizes[T] = (d, ctypes.byref(d), switch_few_workspace_size(d, self._top_k))
         return got
 
     def __call__(self, x, x_scale=None, out=None, ws=None, stream=None):
         """x [T, d] of the experts' type (8-bit experts: bfloat16, or float8_e4m3fn with x_scale [T] float32).
         Returns a dict with y [T, d] float32 (no residual), aux, expert / gate / slot ([T], or [T, 2] with top_k 2)
         and counts.  ``out`` takes the result of an earlier call with as many tokens, which is overwritten."""
-        dev = self.device
+        dev = self._device
         if stream is not None:
             with _under(stream, dev):
                 return self(x, x_scale, out, ws)
-        z = _names or _torch_names()
-        shape, k = x.shape, self.top_k
+        bias, si, so = self._logit_bias, self._w_in_scale, self._w_out_scale
+        held = (self._w_r.data_ptr(), None if bias is None else bias.data_ptr(), self._w_in.data_ptr(),
+                None if si is None else si.data_ptr(), self._w_out.data_ptr(), None if so is None else so.data_ptr())
+        if held != self._held or self._memory is None:
+            # A tensor has other memory than it had: its .data may have been replaced, by something of another size
+            # or type too.  The memory is kept, so that nothing else can come to lie at its address unseen.
+            self._held = held = self._weights()
+            self._memory = [t.detach() for t in (self._w_r, bias, self._w_in, si, self._w_out, so) if t is not None]
+        return self._run(x, x_scale, held, out, ws)
+
+    def _run(self, x, x_scale, held, out, ws):
+        dev, z = self._device, _names or _torch_names()
+        shape, k = x.shape, self._top_k
         if len(shape) != 2:
-            raise ValueError(f"x must be [T, {self.d_model}], got {list(shape)}")
+            raise ValueError(f"x must be [T, {self._d_model}], got {list(shape)}")
         T = shape[0]
-        if x_scale is not None and self.w_in_scale is None:
+        if x_scale is not None and self._w_in_scale is None:
             raise ValueError("x_scale goes with float8_e4m3fn experts and x")
-        px = _want("x", x, (T, self.d_model), self._x_types[x_scale is not None], dev)
+        px = _want("x", x, (T, self._d_model), self._x_types[x_scale is not None], dev)
         pxs = _want("x_scale", x_scale, (T,), z.f32, dev)
         got = self._sizes.get(T)
         d, ref, size = self._dims(T) if got is None else got
@@ -792,11 +812,11 @@ class FewLayer:
 
         def make():
             pairs, f32, i32 = (T,) if k == 1 else (T, k), z.torch.float32, z.torch.int32
-            return dict(y=empty(T, self.d_model, dtype=f32, device=dev), expert=empty(pairs, dtype=i32, device=dev),
+            return dict(y=empty(T, self._d_model, dtype=f32, device=dev), expert=empty(pairs, dtype=i32, device=dev),
                         gate=empty(pairs, dtype=f32, device=dev), slot=empty(pairs, dtype=i32, device=dev),
-                        counts=empty(self.num_experts, dtype=i32, device=dev), aux=empty(1, dtype=f32, device=dev))
+                        counts=empty(self._num_experts, dtype=i32, device=dev), aux=empty(1, dtype=f32, device=dev))
 
-        out = _result(out, ("few", T, k, self.d_model, self.num_experts, dev), make)
+        out = _result(out, ("few", T, k, self._d_model, self._num_experts, dev), make)
         own = out.own
         if ws is None:
             ws = empty(size, dtype=z.torch.uint8, device=dev)
@@ -804,21 +824,26 @@ class FewLayer:
             size = ws.numel() * ws.element_size()
             if ws.device != dev:
                 raise ValueError(f"ws must be on {dev}, got {ws.device}")
-        bias, si, so = self.logit_bias, self.w_in_scale, self.w_out_scale
-        _launch(lib().switch_layer_fwd_few, "switch_layer_fwd_few", dev, ref, k, px, pxs,
-                self.w_r.data_ptr(), None if bias is None else bias.data_ptr(), self.w_in.data_ptr(),
-                None if si is None else si.data_ptr(), self.w_out.data_ptr(), None if so is None else so.data_ptr(),
+        _launch(lib().switch_layer_fwd_few, "switch_layer_fwd_few", dev, ref, k, px, pxs, *held,
                 own["y"].data_ptr(), own["expert"].data_ptr(), own["gate"].data_ptr(), own["slot"].data_ptr(),
                 own["counts"].data_ptr(), own["aux"].data_ptr(), _ptr(ws), size)
         out["capacity"], out["flags"], out["workspace"] = d.capacity, d.flags, ws
         return out
 
 
+for _name in ("w_r", "w_in", "w_out", "logit_bias", "w_in_scale", "w_out_scale", "top_k", "capacity",
+              "capacity_factor", "flags", "num_experts", "d_ff", "d_model", "device", "dtype"):
+    setattr(FewLayer, _name, property(operator.attrgetter("_" + _name)))
+del _name
+
+
 def layer_fwd_few(x, w_r, w_in, w_out, top_k: int = 1, capacity=None, capacity_factor=None, logit_bias=None,
                   x_scale=None, w_in_scale=None, w_out_scale=None, flags: int = 0, ws=None, out=None, stream=None):
     """layer_fwd / layer_fwd_top2 for up to 64 tokens (see FewLayer, which saves the checks of the weights)."""
-    return FewLayer(w_r, w_in, w_out, top_k, capacity, capacity_factor, logit_bias, w_in_scale, w_out_scale, flags)(
-        x, x_scale, out, ws, stream)
+    layer = FewLayer(w_r, w_in, w_out, top_k, capacity, capacity_factor, logit_bias, w_in_scale, w_out_scale, flags)
+    if stream is not None:
+        return layer(x, x_scale, out, ws, stream)
+    return layer._run(x, x_scale, layer._held, out, ws)
 
 
 def block_fwd(residual, norm_weight, w_r, w_in, w_out, delta=None, eps: float = 1e-6, top_k: int = 1, capacity=None,

@@ -71,3 +71,30 @@ def test_blocks_allocate_on_the_stream_that_they_use(monkeypatch):
     sm.block_bwd(f, rows[0], w_r, w_in, w_out, rows, stream="side")
     assert seen == [("layer_bwd", "side", None), ("norm_bwd", "side", None)]
     assert not now
+
+
+def test_a_handle_cannot_be_changed_under_its_plans(monkeypatch):
+    """Sizes and addresses are kept per number of tokens: what they come from cannot be set, and weights that have
+    other memory are checked again before it is read."""
+    checked = sm._want
+    monkeypatch.setattr(sm, "_want", lambda name, t, shape, dtypes, device: None if t is None else t.data_ptr())
+    w_r, w_in, w_out = weights()
+    bias = torch.zeros(N)
+    layer = sm.FewLayer(w_r, w_in, w_out, top_k=2, capacity=3, logit_bias=bias)
+    assert layer.w_in is w_in and layer.logit_bias is bias and layer.top_k == 2 and layer.capacity == 3
+    assert (layer.num_experts, layer.d_ff, layer.d_model, layer.dtype) == (N, F, D, torch.bfloat16)
+    for name in ("w_r", "w_in", "w_out", "logit_bias", "w_in_scale", "w_out_scale", "top_k", "capacity",
+                 "capacity_factor", "flags", "num_experts", "d_ff", "d_model", "device", "dtype"):
+        with pytest.raises(AttributeError):
+            setattr(layer, name, None)
+    assert layer._dims(7)[0].capacity == 3
+    # a call comes to the checks when an address is another one, and stops there
+    monkeypatch.setattr(sm, "_want", lambda name, t, *a: checked(name, t, *a) if name == "w_in" else
+                        None if t is None else t.data_ptr())
+    x = torch.zeros(T, D, dtype=torch.bfloat16)
+    w_in.data = torch.zeros(N, F // 2, D, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="w_in must be"):
+        layer(x)
+    w_in.data = torch.zeros(N, F, D)
+    with pytest.raises(TypeError, match="w_in must be"):
+        layer(x)

@@ -136,3 +136,24 @@ def test_what_relu_removes_takes_no_bits(T, w, d, large):
     y = run(p, 1, T)["y"]
     assert ((y[:, :60].double() - v).abs() <= HELD[w] * 1.01 * v).all()
     assert (y[:, 60:] == 0).all()
+
+
+def test_a_handle_follows_weights_that_move():
+    """.data replaced by the same weights elsewhere: read there.  By others of its kind: those."""
+    p = make(5, 128, 256, 4, "bf16", seed=70)
+    layer = sm.FewLayer(p["w_r"], p["w_in"], p["w_out"], top_k=2)
+    want = layer(p["x"])["y"]
+    old = p["w_in"].data
+    p["w_in"].data = old.clone()
+    assert torch.equal(layer(p["x"])["y"], want)
+    p["w_in"].data = old * 2
+    got = layer(p["x"])["y"]
+    assert torch.equal(got, sm.layer_fwd_few(p["x"], p["w_r"], old * 2, p["w_out"], top_k=2)["y"])
+    p["w_in"].data = old[:, :128].contiguous()
+    with pytest.raises(ValueError):
+        layer(p["x"])
+    p["w_in"].data = old.float()
+    with pytest.raises(TypeError):
+        layer(p["x"])
+    p["w_in"].data = old
+    assert torch.equal(layer(p["x"])["y"], want)
