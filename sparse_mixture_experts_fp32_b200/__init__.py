@@ -850,24 +850,28 @@ def block_fwd(residual, norm_weight, w_r, w_in, w_out, delta=None, eps: float = 
               capacity_factor=None, logit_bias=None, w_in_scale=None, w_out_scale=None, flags: int = 0, stream=None):
     """One pre-norm block: s = residual + delta, x = s / rms(s) * norm_weight, y = layer(x); the caller adds y as
     the next block's delta.  Up to 64 tokens outside of training go through switch_layer_fwd_few (8-bit experts
-    always do, with x in 8 bits), others through switch_layer_fwd / switch_layer_fwd_top2.  Returns the layer's
-    dict with sum (residual where there is no delta), x, x_scale and rstd besides."""
+    always do, with x in 8 bits: more tokens are refused), others through switch_layer_fwd / switch_layer_fwd_top2.
+    Sizes and options that the layer for few tokens cannot run with are refused before the norm is launched.  Returns
+    the layer's dict with sum (residual where there is no delta), x, x_scale and rstd besides."""
     import torch
     if stream is not None:
         with _under(stream, residual.device):
             return block_fwd(residual, norm_weight, w_r, w_in, w_out, delta, eps, top_k, capacity, capacity_factor,
                              logit_bias, w_in_scale, w_out_scale, flags)
-    few = w_in.dtype == torch.float8_e4m3fn or (residual.shape[0] <= SWITCH_FEW_MAX_TOKENS
-                                                and (flags & ~SWITCH_FLAG_SIMT_FFN) == 0)
-    if not few and top_k not in (1, 2):
+    T, e4m3 = residual.shape[0], w_in.dtype == torch.float8_e4m3fn
+    if top_k not in (1, 2):
         raise ValueError("top_k must be 1 or 2")
+    if capacity is None and capacity_factor is None:
+        raise ValueError("give capacity or capacity_factor")
+    if e4m3 and T > SWITCH_FEW_MAX_TOKENS:
+        raise ValueError(f"float8_e4m3fn experts take at most {SWITCH_FEW_MAX_TOKENS} tokens, got {T}")
+    layer = None
+    if e4m3 or (T <= SWITCH_FEW_MAX_TOKENS and (flags & ~SWITCH_FLAG_SIMT_FFN) == 0):
+        layer = FewLayer(w_r, w_in, w_out, top_k, capacity, capacity_factor, logit_bias, w_in_scale, w_out_scale, flags)
     n = norm_fwd(residual, norm_weight, delta=delta, eps=eps, out_dtype=w_in.dtype)
     x = n["out"]
-    if few:
-        if capacity is None and capacity_factor is None:
-            raise ValueError("give capacity or capacity_factor")
-        r = layer_fwd_few(x, w_r, w_in, w_out, top_k, capacity, capacity_factor, logit_bias, n["scale"], w_in_scale,
-                          w_out_scale, flags)
+    if layer is not None:
+        r = layer._run(x, n["scale"], layer._held, None, None)
     else:
         r = (layer_fwd if top_k == 1 else layer_fwd_top2)(x, w_r, w_in, w_out, capacity, capacity_factor, logit_bias,
                                                           flags)

@@ -98,3 +98,21 @@ def test_a_handle_cannot_be_changed_under_its_plans(monkeypatch):
     w_in.data = torch.zeros(N, F, D)
     with pytest.raises(TypeError, match="w_in must be"):
         layer(x)
+
+
+def test_a_block_refuses_before_it_launches(no_calls):
+    """Sizes and options that the layer cannot run with are found before the norm is launched."""
+    w_r, w_in, w_out = weights()
+    rows, nw = torch.zeros(65, D), torch.ones(D)
+    e_in, e_out = w_in.to(torch.float8_e4m3fn), w_out.to(torch.float8_e4m3fn)
+    scales = dict(w_in_scale=torch.ones(N, F), w_out_scale=torch.ones(N, D))
+    with pytest.raises(ValueError, match="at most 64 tokens, got 65"):
+        sm.block_fwd(rows, nw, w_r, e_in, e_out, capacity=8, **scales)
+    with pytest.raises(ValueError, match="have w_in_scale and w_out_scale"):
+        sm.block_fwd(rows[:8], nw, w_r, e_in, e_out, capacity=8)
+    for t in (8, 65):
+        with pytest.raises(ValueError, match="give capacity"):
+            sm.block_fwd(rows[:t], nw, w_r, w_in, w_out)
+        for k in (0, 3):
+            with pytest.raises(ValueError, match="top_k must be 1 or 2"):
+                sm.block_fwd(rows[:t], nw, w_r, w_in, w_out, capacity=8, top_k=k)
