@@ -576,8 +576,20 @@ def _want(name, t, shape, dtypes, device):
 
 class _Result(dict):
     """A result that a later call of the same sizes may write into again (out=): the tensors of its first call,
-    whatever the dict holds by then."""
-    __slots__ = ("key", "own")
+    whatever the dict holds by then.  They may not be inputs of that call, other than where it says so."""
+    __slots__ = ("key", "own", "addresses")
+
+    def holds(self, *inputs):
+        """Whether one of the inputs' addresses is one of the tensors'."""
+        if self.addresses is None:
+            self.addresses = frozenset(t.data_ptr() for t in self.own.values() if t is not None)
+        return not self.addresses.isdisjoint(inputs)
+
+    def refuse(self, **inputs):
+        """Raises where an input is one of the tensors."""
+        for name, address in inputs.items():
+            if address and address in self.addresses:
+                raise ValueError(f"{name} is a tensor of the result given as out, which the call overwrites")
 
 
 def _result(out, key, make):
@@ -585,7 +597,7 @@ def _result(out, key, make):
     if out is None:
         own = make()
         out = _Result(own)
-        out.key, out.own = key, own
+        out.key, out.own, out.addresses = key, own, None
     elif type(out) is not _Result or out.key != key:
         raise ValueError("out must be the result of an earlier call of the same function, sizes, types and device")
     else:
@@ -629,7 +641,8 @@ def norm_fwd(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None, in
     residual [T, d] float32 or bfloat16; delta [T, d] float32 or bfloat16 (a layer's y), or None for s = residual;
     weight [d] float32; out_dtype float32, bfloat16 or float8_e4m3fn (default: residual's).  Returns a dict with
     sum (None without a delta; residual itself with ``inplace``), out, scale ([T], 8-bit outputs only) and rstd [T].
-    ``out`` takes the result of an earlier call of the same sizes, which is overwritten."""
+    ``out`` takes the result of an earlier call of the same sizes, which is overwritten: no input may be a part of
+    it, but its sum may be residual."""
     shape, dev = _rows("residual", residual)
     if stream is not None:
         with _under(stream, dev):
@@ -644,15 +657,18 @@ def norm_fwd(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None, in
     pw = _want("weight", weight, (dm,), z.f32, dev)
     stored = delta is not None and not inplace
     key = ("norm_fwd", shape, dtype, out_dtype, stored, dev)
-    if out is None or type(out) is not _Result or out.key != key:
+    reuse = out is not None
+    if not reuse or type(out) is not _Result or out.key != key:
         empty, f32 = z.torch.empty, z.torch.float32
         out = _result(out, key, lambda: dict(
             sum=z.torch.empty_like(residual) if stored else None, out=empty(shape, dtype=out_dtype, device=dev),
             scale=empty(T, dtype=f32, device=dev) if out_dtype == z.e4m3 else None,
             rstd=empty(T, dtype=f32, device=dev)))
     own = out.own
-    out.update(own)
     total, scale, codes = own["sum"], own["scale"], z.codes
+    if reuse and out.holds(pr, pd, pw):  # sum may be residual itself
+        out.refuse(residual=None if total is not None and pr == total.data_ptr() else pr, delta=pd, weight=pw)
+    out.update(own)
     if total is not None:
         ps = total.data_ptr()
     elif delta is not None:
@@ -675,7 +691,9 @@ def _norm_bwd_dims(T, d_model, code):
 def norm_bwd(sum, weight, rstd, dout, dsum=None, out=None, stream=None):
     """Gradient of norm_fwd (switch_norm_bwd): from dout [T, d] float32 (the gradient of its out) and dsum [T, d]
     float32 (the gradient of its sum from elsewhere, or None), dresidual [T, d] (of residual and of delta alike) and
-    dweight [d], float32.  sum is norm_fwd's sum, or residual where there was no delta."""
+    dweight [d], float32.  sum is norm_fwd's sum, or residual where there was no delta.  ``out`` takes the result of
+    an earlier call of the same sizes, which is overwritten: its dresidual may be dout or dsum, no other input a part
+    of it."""
     shape, dev = _rows("sum", sum)
     if stream is not None:
         with _under(stream, dev):
@@ -686,10 +704,13 @@ def norm_bwd(sum, weight, rstd, dout, dsum=None, out=None, stream=None):
     ps, pw = _want("sum", sum, shape, z.floats, dev), _want("weight", weight, (dm,), f32, dev)
     pr, pg, pu = (_want("rstd", rstd, (T,), f32, dev), _want("dout", dout, shape, f32, dev),
                   _want("dsum", dsum, shape, f32, dev))
-    empty = z.torch.empty
+    empty, reuse = z.torch.empty, out is not None
     out = _result(out, ("norm_bwd", shape, dev), lambda: dict(
         dresidual=empty(shape, dtype=f32[0], device=dev), dweight=empty(dm, dtype=f32[0], device=dev)))
     own = out.own
+    if reuse and out.holds(ps, pw, pr, pg, pu):
+        at = own["dresidual"].data_ptr()
+        out.refuse(sum=ps, weight=pw, rstd=pr, dout=None if pg == at else pg, dsum=None if pu == at else pu)
     _, ref, size = _norm_bwd_dims(T, dm, z.codes[sum.dtype])
     ws = empty(size, dtype=z.torch.uint8, device=dev)
     _launch(lib().switch_norm_bwd, "switch_norm_bwd", dev, ref, ps, pw, pr, pg, pu,
@@ -699,7 +720,8 @@ def norm_bwd(sum, weight, rstd, dout, dsum=None, out=None, stream=None):
 
 def quantize_rows(x, out=None, stream=None):
     """x [..., cols] float32 or bfloat16 in 8 bits (switch_quantize_rows): a dict with q (float8_e4m3fn, x's shape)
-    and scale (float32, x's shape without the last dimension); x is about q * scale."""
+    and scale (float32, x's shape without the last dimension); x is about q * scale.  ``out`` takes the result of an
+    earlier call of the same sizes, which is overwritten: x may not be a part of it."""
     if not x.is_cuda:
         raise TypeError("switch_moe tensors must be CUDA tensors")
     shape, dev = x.shape, x.device
@@ -713,10 +735,12 @@ def quantize_rows(x, out=None, stream=None):
     for n in shape[:-1]:
         rows *= n
     px = _want("x", x, shape, z.floats, dev)
-    empty = z.torch.empty
+    empty, reuse = z.torch.empty, out is not None
     out = _result(out, ("quantize_rows", shape, dev), lambda: dict(
         q=empty(shape, dtype=z.e4m3, device=dev), scale=empty(shape[:-1], dtype=z.torch.float32, device=dev)))
     own = out.own
+    if reuse and out.holds(px):
+        out.refuse(x=px)
     _launch(lib().switch_quantize_rows, "switch_quantize_rows", dev, rows, shape[-1], z.codes[x.dtype], px,
             own["q"].data_ptr(), own["scale"].data_ptr())
     return out
@@ -781,7 +805,8 @@ class FewLayer:
     def __call__(self, x, x_scale=None, out=None, ws=None, stream=None):
         """x [T, d] of the experts' type (8-bit experts: bfloat16, or float8_e4m3fn with x_scale [T] float32).
         Returns a dict with y [T, d] float32 (no residual), aux, expert / gate / slot ([T], or [T, 2] with top_k 2)
-        and counts.  ``out`` takes the result of an earlier call with as many tokens, which is overwritten."""
+        and counts.  ``out`` takes the result of an earlier call with as many tokens, which is overwritten: no input may
+        be a part of it."""
         dev = self._device
         if stream is not None:
             with _under(stream, dev):
@@ -808,7 +833,7 @@ class FewLayer:
         pxs = _want("x_scale", x_scale, (T,), z.f32, dev)
         got = self._sizes.get(T)
         d, ref, size = self._dims(T) if got is None else got
-        empty = z.torch.empty
+        empty, reuse = z.torch.empty, out is not None
 
         def make():
             pairs, f32, i32 = (T,) if k == 1 else (T, k), z.torch.float32, z.torch.int32
@@ -818,6 +843,8 @@ class FewLayer:
 
         out = _result(out, ("few", T, k, self._d_model, self._num_experts, dev), make)
         own = out.own
+        if reuse and out.holds(px, pxs):
+            out.refuse(x=px, x_scale=pxs)
         if ws is None:
             ws = empty(size, dtype=z.torch.uint8, device=dev)
         else:

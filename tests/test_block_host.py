@@ -116,3 +116,44 @@ def test_a_block_refuses_before_it_launches(no_calls):
         for k in (0, 3):
             with pytest.raises(ValueError, match="top_k must be 1 or 2"):
                 sm.block_fwd(rows[:t], nw, w_r, w_in, w_out, capacity=8, top_k=k)
+
+
+@pytest.fixture
+def on_the_host(monkeypatch):
+    """The Python of the calls on CPU tensors, up to the launch."""
+    launched = []
+    monkeypatch.setattr(sm, "_rows", lambda name, t: (t.shape, t.device))
+    monkeypatch.setattr(sm, "_want", lambda name, t, *a: None if t is None else t.data_ptr())
+    monkeypatch.setattr(sm, "_ptr", lambda t: None if t is None else t.data_ptr())
+    monkeypatch.setattr(sm, "_launch", lambda fn, where, *a: launched.append(where))
+    return launched
+
+
+def test_an_input_may_not_be_a_tensor_of_the_result_that_is_overwritten(on_the_host):
+    x, w = torch.ones(T, D), torch.ones(D)
+    r = sm.norm_fwd(x, w, delta=x.clone())
+    sm.norm_fwd(x, w, delta=x, out=r)
+    sm.norm_fwd(r["sum"], w, delta=x, out=r)  # sum may be residual
+    for bad in (dict(residual=r["out"], delta=x), dict(residual=x, delta=r["out"]), dict(residual=x, delta=r["sum"])):
+        with pytest.raises(ValueError, match="result given as out"):
+            sm.norm_fwd(weight=w, out=r, **bad)
+    g = sm.norm_bwd(x, w, torch.ones(T), x.clone())
+    sm.norm_bwd(x, w, torch.ones(T), g["dresidual"], out=g)  # dresidual may be dout or dsum
+    sm.norm_bwd(x, w, torch.ones(T), x.clone(), dsum=g["dresidual"], out=g)
+    for bad in (dict(sum=g["dresidual"], weight=w), dict(sum=x, weight=g["dweight"])):
+        with pytest.raises(ValueError, match="result given as out"):
+            sm.norm_bwd(rstd=torch.ones(T), dout=x.clone(), out=g, **bad)
+    layer = sm.FewLayer(*weights(torch.float32))
+    y = layer(x)
+    layer(x, out=y)
+    before = len(on_the_host)
+    with pytest.raises(ValueError, match="x is a tensor of the result"):
+        layer(y["y"], out=y)
+    e = torch.float8_e4m3fn
+    layer = sm.FewLayer(*weights(e), w_in_scale=torch.ones(N, F), w_out_scale=torch.ones(N, D))
+    y = layer(x.to(e), x_scale=torch.ones(T))
+    with pytest.raises(ValueError, match="x_scale is a tensor of the result"):
+        layer(x.to(e), x_scale=y["gate"], out=y)
+    assert len(on_the_host) == before + 1
+    empty = sm.norm_fwd(x[:0], w, delta=x[:0])
+    sm.norm_fwd(x[:0], w, delta=x[:0], out=empty)
