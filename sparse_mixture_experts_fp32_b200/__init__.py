@@ -621,6 +621,8 @@ def _under(stream, device):
     """Makes `stream` (a torch stream or a cudaStream_t) the current one, so that what is allocated meanwhile is
     ordered on the stream that it is used on."""
     import torch
+    if not isinstance(stream, int) and stream.device != device:
+        raise ValueError(f"stream must be on {device}, got {stream.device}")
     return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
 
 

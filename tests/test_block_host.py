@@ -157,3 +157,20 @@ def test_an_input_may_not_be_a_tensor_of_the_result_that_is_overwritten(on_the_h
     assert len(on_the_host) == before + 1
     empty = sm.norm_fwd(x[:0], w, delta=x[:0])
     sm.norm_fwd(x[:0], w, delta=x[:0], out=empty)
+
+
+def test_a_stream_of_another_device_is_refused(on_the_host):
+    """(Made current, it would change the device, and the call would go to some other stream of its own one.)"""
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    x, w = torch.ones(T, D), torch.ones(D)
+    calls = (lambda s: sm.norm_fwd(x, w, stream=s), lambda s: sm.norm_bwd(x, w, torch.ones(T), x, stream=s),
+             lambda s: sm.block_fwd(x, w, *weights(), capacity=T, stream=s),
+             lambda s: sm.FewLayer(*weights(torch.float32))(x, stream=s),
+             lambda s: sm.layer_fwd_few(x, *weights(torch.float32), stream=s),
+             lambda s: sm.block_bwd(dict(expert=x[:, 0]), w, *weights(), x, stream=s))
+    for call in calls:
+        with pytest.raises(ValueError, match="stream must be on"):
+            call(Stream())
+    assert not on_the_host
