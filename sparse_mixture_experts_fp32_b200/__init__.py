@@ -626,6 +626,12 @@ def _under(stream, device):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
 
 
+def _current(device):
+    """Makes `device` the current one, for the calls that go by it (those above do so themselves)."""
+    import torch
+    return torch.cuda.device(device)
+
+
 def _rows(name, t):
     """Shape and device of a [rows, columns] CUDA tensor."""
     shape = t.shape
@@ -902,8 +908,9 @@ def block_fwd(residual, norm_weight, w_r, w_in, w_out, delta=None, eps: float = 
     if layer is not None:
         r = layer._run(x, n["scale"], layer._held, None, None)
     else:
-        r = (layer_fwd if top_k == 1 else layer_fwd_top2)(x, w_r, w_in, w_out, capacity, capacity_factor, logit_bias,
-                                                          flags)
+        with _current(x.device):
+            r = (layer_fwd if top_k == 1 else layer_fwd_top2)(x, w_r, w_in, w_out, capacity, capacity_factor,
+                                                              logit_bias, flags)
     return dict(r, sum=residual if delta is None else n["sum"], x=x, x_scale=n["scale"], rstd=n["rstd"])
 
 
@@ -915,6 +922,7 @@ def block_bwd(fwd: dict, norm_weight, w_r, w_in, w_out, dy, dsum=None, g_aux: fl
     if stream is not None:
         with _under(stream, dy.device):  # dx, which dies here, is allocated on the stream that it is used on
             return block_bwd(fwd, norm_weight, w_r, w_in, w_out, dy, dsum, g_aux, logit_bias)
-    g = layer_bwd(fwd, fwd["x"], w_r, w_in, w_out, dy, g_aux, logit_bias)
+    with _current(dy.device):
+        g = layer_bwd(fwd, fwd["x"], w_r, w_in, w_out, dy, g_aux, logit_bias)
     n = norm_bwd(fwd["sum"], norm_weight, fwd["rstd"], g.pop("dx"), dsum=dsum)
     return dict(g, dresidual=n["dresidual"], dnorm_weight=n["dweight"])

@@ -1,4 +1,6 @@
 """block_fwd, block_bwd and FewLayer without a GPU: what they refuse, and before any device work."""
+import contextlib
+
 import pytest
 import torch
 
@@ -20,7 +22,8 @@ def no_calls(monkeypatch):
     monkeypatch.setattr(sm, "lib", lambda: Library())
 
 
-def test_gradients_of_a_top2_forward_are_refused(no_calls):
+def test_gradients_of_a_top2_forward_are_refused(no_calls, monkeypatch):
+    monkeypatch.setattr(sm, "_current", lambda device: contextlib.nullcontext())
     w_r, w_in, w_out = weights()
     x, dy = torch.zeros(T, D, dtype=torch.bfloat16), torch.zeros(T, D)
     two = torch.zeros(T, 2, dtype=torch.int32)
@@ -58,6 +61,7 @@ def test_blocks_allocate_on_the_stream_that_they_use(monkeypatch):
     w_r, w_in, w_out = weights()
     x, rows = torch.zeros(100, D, dtype=torch.bfloat16), torch.zeros(100, D)
     monkeypatch.setattr(sm, "_under", under)
+    monkeypatch.setattr(sm, "_current", lambda device: contextlib.nullcontext())
     monkeypatch.setattr(sm, "norm_fwd", record("norm_fwd", dict(out=x, scale=None, sum=rows, rstd=rows[:, 0])))
     monkeypatch.setattr(sm, "norm_bwd", record("norm_bwd", dict(dresidual=rows, dweight=rows[0])))
     monkeypatch.setattr(sm, "layer_bwd", record("layer_bwd", dict(dx=rows)))
@@ -174,3 +178,27 @@ def test_a_stream_of_another_device_is_refused(on_the_host):
         with pytest.raises(ValueError, match="stream must be on"):
             call(Stream())
     assert not on_the_host
+
+
+def test_blocks_of_another_device_than_the_current_one(monkeypatch):
+    """The layer's calls go by the current device: it is that of the tensors meanwhile."""
+    now, seen = [], []
+
+    @contextlib.contextmanager
+    def current(device):
+        now.append(device)
+        yield
+        now.pop()
+
+    w_r, w_in, w_out = weights()
+    x, rows = torch.zeros(100, D, dtype=torch.bfloat16), torch.zeros(100, D)
+    monkeypatch.setattr(sm, "_current", current)
+    monkeypatch.setattr(sm, "norm_fwd", lambda *a, **k: dict(out=x, scale=None, sum=rows, rstd=rows[:, 0]))
+    monkeypatch.setattr(sm, "norm_bwd", lambda *a, **k: dict(dresidual=rows, dweight=rows[0]))
+    monkeypatch.setattr(sm, "layer_bwd", lambda *a, **k: seen.append(list(now)) or dict(dx=rows))
+    for name in ("layer_fwd", "layer_fwd_top2"):
+        monkeypatch.setattr(sm, name, lambda *a, **k: seen.append(list(now)) or dict(y=rows))
+    f = sm.block_fwd(rows, rows[0], w_r, w_in, w_out, capacity=8)
+    sm.block_fwd(rows, rows[0], w_r, w_in, w_out, capacity=8, top_k=2)
+    sm.block_bwd(f, rows[0], w_r, w_in, w_out, rows)
+    assert seen == [[rows.device]] * 3 and not now
