@@ -326,9 +326,9 @@ switch_status_t switch_layer_bwd(const switch_dims_t *dims, const void *x, const
  *  - the hidden activations are not rounded to bfloat16: y carries float32
  *    rounding only (about 1e-6 relative) beyond that of the given inputs
  *    (8-bit experts on tensor cores: a bfloat16 x below 2^-29 of its token's
- *    largest |x| is rounded to 2^-37 of that; a hidden value to 2^-19 of
- *    itself, or where that is more to 2^-33 of the largest value of its row, as
- *    the partial sums give it that long rows are added from);
+ *    largest |x| is held within 2^-36 of that; a hidden value within 2^-19 of
+ *    itself, or where that is more within 2^-32 of the largest value of its row,
+ *    as the partial sums give it that long rows are added from);
  *  - the experts may be SWITCH_E4M3 (dims.dtype), with a float32 scale per
  *    output row (w_in_scale [N, F], w_out_scale [N, d]: W = q * scale); x is
  *    then bfloat16, or SWITCH_E4M3 too, with a scale per token (x_scale [T]).

@@ -197,7 +197,8 @@ __device__ __forceinline__ float unscale(int k) { return k == 1000 ? __int_as_fl
 // 16 bfloat16 values below 2^15 -> three rows of 16 e5m2 bytes, term i holding
 // what the terms before it left, times 8^i.  They are cut in float16, two values
 // at a time, which holds every difference exactly: all of the 8 bits of a value
-// down to 2^-15, and 2^-23 of any smaller one.
+// down to 2^-15; a smaller one is off by half of the third term's smallest step,
+// 2^-23, and half of float16's, 2^-25: less than 2^-36 of a row's largest.
 __device__ __forceinline__ void store_e5m2_terms(uint8_t *tile, int row0, int chunk, const float (&v)[16]) {
     uint32_t w[3][4];
 #pragma unroll
@@ -225,8 +226,9 @@ __device__ __forceinline__ void store_e5m2_terms(uint8_t *tile, int row0, int ch
 // values at a time: its 11 bits are what three terms hold, down to values of 2^-7
 // (below, the third term is at the end of e4m3's range and leaves some); what it
 // leaves of v and what they leave of it, times 16^3, make the fourth and fifth.
-// So a value is off by 2^-19 of itself, or by half of the fifth term's smallest
-// step, 2^-26 (2^-33 of a row's largest), where that is more.
+// So a value is off by 2^-19 of itself, or where that is more by half of the
+// fifth term's smallest step, 2^-26, and half of float16's where the fourth
+// begins, 2^-29: less than 2^-32 of a row's largest.
 __device__ __forceinline__ void store_e4m3_terms(uint8_t *tile, int row0, int chunk, const float (&v)[16]) {
     constexpr int TERMS = 5;
     uint32_t w[TERMS][4];
