@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(1024)
     norm_fwd_kernel(const R *residual, const D *delta, const float *__restrict__ weight, R *sum, O *out,
                     float *__restrict__ scale, float *__restrict__ rstd, int64_t T, int d, float eps) {
     constexpr bool kDelta = !std::is_same<D, None>::value;
-    __shared__ float part[2][32];
+    __shared__ float part[3][32];
     const int tpr = blockDim.x;
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = t < T;
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(1024)
         uint32_t top = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(s[k]) & 0x7fffffffu);
-        top = row_max(top, tpr, part[1]);
+        top = row_max(top, tpr, part[2]);
         if (top < 0x7f800000u) {  // (a row with a NaN or an infinity stays as it is)
             const float m = fmaxf(__uint_as_float(top), __fsqrt_rn(eps));
             const int down = m > 0.f ? -ilogbf(m) : 0;
