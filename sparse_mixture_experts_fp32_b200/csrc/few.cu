@@ -62,8 +62,9 @@ __device__ __forceinline__ void load_elems(const T *p, float (&v)[V]) {
 // ---------------------------------------------------------------------------
 // router
 // ---------------------------------------------------------------------------
-// Four warps of 64 registers: a block fits beside one of the second kernel's on an SM, so that those
-// start, and the next call's routers with them, before the others end.
+// Four warps of 64 registers: a block fits beside one of the second kernel's on an SM, so that neither
+// kernel has to wait for the other's last block.  (In a graph the second kernel's blocks start within
+// 0.5 us of the last router's end and are past their wait after 0.8 us.)
 constexpr int kRouterThreads = 128;
 
 // Block (i, j): the logits of TE experts for TT tokens, the dot products
@@ -204,8 +205,9 @@ __device__ __forceinline__ float sum8(float (&v)[8], int lane) {
 // red[j * 8 + r] = sum_k w[r][k] x_j[k], x_j the row token[j] (or j) of `in`,
 // over this warp's share of k (steps first, first + TEAM, ... of 32 V elements),
 // for kSimtRows rows of weights and m <= TOK tokens; rows past `rows_left`
-// repeat the last one.  U steps' weights are in flight together, as many as the
-// registers beside the accumulators hold.
+// repeat the last one.  U steps' weights are in flight together, about as many as
+// the registers beside the accumulators hold (19 of the 20 forms spill 42 to 262
+// bytes; only that of odd sizes, four tokens and long rows does not).
 template <typename W, typename X, int V, int TOK, int TEAM>
 __device__ __forceinline__ void simt_dots(const W *w, int rows_left, int K, const X *in, const int *token, int m,
                                           int pitch, int first, int lane, float *red) {

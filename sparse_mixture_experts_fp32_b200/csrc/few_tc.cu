@@ -35,11 +35,12 @@
 // An item is a tile of 128 weight rows of one expert, cut along its length into
 // equal parts when there are few tiles (few_splits).
 //
-// Measured on a B200 (whole call in a graph; copy bandwidth 6549 GB/s): 32 tokens
-// top-2, 128 bfloat16 experts of 1024 x 4096 151 us (85 % of it), 8 tokens, 64
-// 8-bit experts of 4096 x 10240 120 us (81 %): bound by the weights' stream.  One
-// token 15.5 us, 48 tokens top-2 on 8 8-bit experts of 768 x 2048 35 us: bound by
-// latency (decisions, first weights, the hand-over of h, y from its parts).
+// Measured on B200s (whole call in a graph; copy bandwidth 6549 GB/s): 32 tokens
+// top-2, 128 bfloat16 experts of 1024 x 4096 152 us (85 % of it), 8 tokens, 64
+// 8-bit experts of 4096 x 10240 122 us (79 %): bound by the weights' stream.  One
+// token 15.5-16.2 us, 48 tokens top-2 on 8 8-bit experts of 768 x 2048 35.8 us:
+// bound by latency (decisions, first weights, the hand-over of h, y from its
+// parts), the last by the block that forms y last.
 #include <cuda.h>
 
 #include <atomic>

@@ -21,10 +21,12 @@
 // maxima are taken on the bit patterns of |v|, whose order is that of the values
 // and puts NaN on top, so that a row with a NaN gets a NaN scale.
 //
-// Measured on a B200 (copy bandwidth 6549 GB/s): 131072 x 1024 bfloat16 +
-// float32 -> bfloat16 194 us (6.9 TB/s), its gradient 304 us (6.2 TB/s);
+// Measured on B200s (copy bandwidth 6549 GB/s): 131072 x 1024 bfloat16 +
+// float32 -> bfloat16 193 us (7.0 TB/s), its gradient 304-312 us (6.0-6.2 TB/s);
 // 8192 x 768 float32 + float32 -> 8 bits 16.2 us (5.0 TB/s); 131072 x 1024
-// bfloat16 to 8 bits 81 us (5.0 TB/s).
+// bfloat16 to 8 bits 81-84 us (4.8-5.0 TB/s).  At widths that are no multiple of
+// 8 (1001) 152 us for 65536 rows to bfloat16 (4.3 TB/s), 113 us from bfloat16 to
+// 8 bits (1.7 TB/s): a row's ends go one by one, in a form of 71 registers.
 #include <cuda_fp8.h>
 
 #include <cfloat>
