@@ -648,7 +648,8 @@ def norm_fwd(residual, weight, delta=None, eps: float = 1e-6, out_dtype=None, in
 
     residual [T, d] float32 or bfloat16; delta [T, d] float32 or bfloat16 (a layer's y), or None for s = residual;
     weight [d] float32; out_dtype float32, bfloat16 or float8_e4m3fn (default: residual's).  Returns a dict with
-    sum (None without a delta; residual itself with ``inplace``, which delta may then not overlap), out, scale ([T], 8-bit outputs only) and rstd [T].
+    sum (None without a delta; residual itself with ``inplace``, which delta may then not overlap), out, scale ([T],
+    8-bit outputs only) and rstd [T].
     ``out`` takes the result of an earlier call of the same sizes, which is overwritten: no input may be a part of
     it, but its sum may be residual."""
     shape, dev = _rows("residual", residual)
